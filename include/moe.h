@@ -17,6 +17,9 @@
  *     moe_expert_ffn    per-expert two-layer GeLU FFN on the packed rows (grouped GEMMs)
  *     moe_combine       gate-weighted sum of the kept expert rows plus the residual terms
  *     moe_layer_forward all of the above (plus the optional PR-MoE dense MLP branch)
+ * and beside them
+ *     moe_gated_ffn     the gated (SwiGLU / GEGLU) expert FFN on the packed rows, with its backward
+ *     moe_grad_norm     the global norm of a list of gradients; moe_clip_grads scales by it
  *
  * Conventions (every entry point):
  *   - Tensor pointers are caller-owned DEVICE memory, row-major, 16-byte aligned. The
@@ -396,6 +399,93 @@ moe_status moe_layer_forward_train(const moe_layer_args* args, void* out, moe_la
 moe_status moe_layer_backward(const moe_layer_args* args, const void* d_out, float aux_weight,
                               float z_weight, moe_layer_grads* grads, void* ws, size_t ws_bytes,
                               moe_stream_t stream);
+
+/* ---------------------------------------------------------------- gated expert FFN
+ * The gated form of the expert feed-forward network (SwiGLU, GEGLU): for every expert e and every
+ * packed row r in [expert_offsets[e], expert_offsets[e+1])
+ *     zg = w_gate[e] x_packed[r,:] + b_gate[e]        zu = w_up[e] x_packed[r,:] + b_up[e]
+ *     h[r,:] = act(zg) * zu                           (elementwise)
+ *     y[r,:] = w_down[e] h[r,:] + b_down[e]
+ * with act(z) = z / (1 + e^-z) (MOE_GATE_SILU) or z Phi(z) (MOE_GATE_GELU, the erf form). It takes
+ * moe_dispatch's packed rows and offsets and its fp32 y is what moe_combine reads; with E = 1 and
+ * expert_offsets = {0, T} it is a dense gated MLP.
+ *
+ * w_gate, w_up: [E, d_ff, d_model]; w_down: [E, d_model, d_ff]; b_gate, b_up: [E, d_ff] or NULL;
+ * b_down: [E, d_model] or NULL; all in dtype. x_packed: [rows_max, d_model] in dtype.
+ * h_packed: [rows_max, d_ff] in dtype (bf16 rounds h, the second product's operand).
+ * y_packed: [rows_max, d_model] in out_dtype (fp32 layers: MOE_F32 only).
+ * saved: NULL, or [2, rows_max, d_ff] in dtype for the backward pass: plane 0 receives act(zg),
+ * plane 1 zu act'(zg).
+ * Rows outside every segment are neither read nor written. Offsets that are not non-decreasing
+ * within [0, rows_max] set MOE_DEVERR_BAD_OFFSETS. capacity_hint: an upper bound on the rows of
+ * any one expert (normally C); it selects tile sizes and how sums are split, so it may change
+ * results in their rounding, and is otherwise free to be wrong.
+ * Limits: those of moe_expert_ffn (bf16: d_model and d_ff multiples of 8). bf16 runs on tcgen05
+ * tensor cores (fp32 accumulate), fp32 on fp32 FMA (no TF32). */
+typedef enum { MOE_GATE_SILU = 0, MOE_GATE_GELU = 1 } moe_gate_act;
+typedef struct {
+  const void* x_packed;
+  const int32_t* expert_offsets; /* [E+1] */
+  int E;
+  int64_t rows_max;
+  int d_model, d_ff;
+  moe_dtype dtype;     /* x, weights, biases, h, saved */
+  moe_dtype out_dtype; /* y_packed */
+  int act;             /* moe_gate_act */
+  const void *w_gate, *b_gate, *w_up, *b_up, *w_down, *b_down;
+  int64_t capacity_hint;
+} moe_gated_ffn_args;
+moe_status moe_gated_ffn_workspace_bytes(size_t* bytes);
+moe_status moe_gated_ffn(const moe_gated_ffn_args* args, void* h_packed, void* y_packed,
+                         void* saved, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The backward pass of moe_gated_ffn, by the chain rule: from dy_packed [rows_max, d_model] (in
+ * args.dtype), and h_packed and saved as the forward call left them,
+ *     dh = dy w_down[e],  du = dh act(zg),  dg = dh zu act'(zg),
+ *     dx = dg w_gate[e] + du w_up[e],
+ *     dw_down[e] = dy^T h,  dw_gate[e] = dg^T x,  dw_up[e] = du^T x   (sums over e's rows),
+ *     db_down, db_gate, db_up: the column sums of dy, dg, du.
+ * Gradients are overwritten; experts without rows get zeros. dx_packed [rows_max, d_model] in
+ * dx_dtype (rows outside every segment are not written); the weight and bias gradients in
+ * grad_dtype, in the parameters' shapes; bias gradients may be NULL (not computed). fp32 layers
+ * take MOE_F32 for both types. bf16 layers round dg and du to bf16 (the operands of the products
+ * that follow) and accumulate in fp32. */
+typedef struct {
+  void* dx_packed;
+  void *dw_gate, *dw_up, *dw_down;
+  void *db_gate, *db_up, *db_down; /* or NULL */
+  moe_dtype dx_dtype;
+  moe_dtype grad_dtype;
+} moe_gated_ffn_grads;
+moe_status moe_gated_ffn_backward_workspace_bytes(const moe_gated_ffn_args* args, size_t* bytes);
+moe_status moe_gated_ffn_backward(const moe_gated_ffn_args* args, const void* dy_packed,
+                                  const void* h_packed, const void* saved,
+                                  const moe_gated_ffn_grads* grads, void* ws, size_t ws_bytes,
+                                  moe_stream_t stream);
+
+/* ---------------------------------------------------------------- gradient norm and clipping
+ * moe_grad_norm: *norm (fp32, device) = the 2-norm of all elements of all tensors together.
+ * moe_clip_grads: out = grad * min(1, max_norm / (*norm + 1e-6)), elementwise over all tensors, in
+ * fp32 with one rounding to out's type; a NaN norm makes every output NaN. Between the two calls a
+ * data-parallel caller can join the norms of several GPUs.
+ * Tensors are contiguous, aligned to their element (2 or 4 bytes; no 16-byte rule here), of any
+ * length >= 0 (below 2^43), fp32 or bf16 each; the list itself is host memory, read during the call.
+ * out may be grad (same type) to clip in place; otherwise no output may overlap another tensor of
+ * the list, so a tensor that is listed twice cannot be clipped (MOE_ERR_INVALID_ARGUMENT).
+ * max_norm must be finite and >= 0. moe_grad_norm ignores out and out_dtype. Results do not change
+ * from call to call. ws: its status block must have been zeroed once (moe_workspace_reset); it
+ * holds the blocks' counter, so two captured graphs that share it must not run at once either. */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t n;
+  moe_dtype dtype, out_dtype;
+} moe_grad_tensor;
+moe_status moe_grad_norm_workspace_bytes(size_t* bytes);
+moe_status moe_grad_norm(const moe_grad_tensor* tensors, int64_t n_tensors, float* norm, void* ws,
+                         size_t ws_bytes, moe_stream_t stream);
+moe_status moe_clip_grads(const moe_grad_tensor* tensors, int64_t n_tensors, const float* norm,
+                          float max_norm, moe_stream_t stream);
 
 /* ---------------------------------------------------------------- status block
  * moe_workspace_reset: zeroes the status block (asynchronous on stream).

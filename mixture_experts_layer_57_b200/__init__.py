@@ -10,4 +10,6 @@ binding. Build with ``python -m mixture_experts_layer_57_b200.build``.
 from . import moe  # noqa: F401
 from .moe import (MoEError, moe_capacity, moe_combine, moe_dispatch, moe_expert_ffn,  # noqa: F401
                   moe_get_device_error, moe_layer_forward, moe_layer_workspace_bytes,
-                  moe_packed_rows_max, moe_router_topk, moe_workspace_reset, layer_args)
+                  moe_packed_rows_max, moe_router_topk, moe_workspace_reset, layer_args,
+                  gated_ffn_args, moe_gated_ffn, moe_gated_ffn_backward, moe_grad_norm,
+                  moe_clip_grads, moe_clip_grad_norm)

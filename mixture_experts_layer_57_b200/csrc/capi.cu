@@ -6,6 +6,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <utility>
+#include <vector>
 
 #include "kernels.h"
 
@@ -1319,6 +1320,270 @@ moe_status moe_layer_backward(const moe_layer_args* args, const void* d_out, flo
                               moe_stream_t stream) {
   if (!args) return MOE_ERR_INVALID_ARGUMENT;
   return backward_impl(args, d_out, aux_weight, z_weight, grads, ws, ws_bytes, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- gated expert FFN
+
+namespace {
+
+moe_status check_gated(const moe_gated_ffn_args* a) {
+  const moe_status st = check_ffn_shape(a->E, a->rows_max, a->d_model, a->d_ff, a->dtype);
+  if (st != MOE_OK) return st;
+  if (!valid_dtype(a->out_dtype) || (a->act != MOE_GATE_SILU && a->act != MOE_GATE_GELU))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (a->dtype == MOE_F32 && a->out_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_gated_pointers(const moe_gated_ffn_args* a, const void* ws) {
+  if (a->capacity_hint < 0 || !a->expert_offsets || !a->w_gate || !a->w_up || !a->w_down || !ws)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (a->rows_max > 0 && !a->x_packed) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned16(a->x_packed) || !aligned16(a->expert_offsets) || !aligned16(a->w_gate) ||
+      !aligned16(a->b_gate) || !aligned16(a->w_up) || !aligned16(a->b_up) ||
+      !aligned16(a->w_down) || !aligned16(a->b_down) || ((uintptr_t)ws % kAlign) != 0)
+    return MOE_ERR_MISALIGNED;
+  return MOE_OK;
+}
+
+GatedFfn gated_of(const moe_gated_ffn_args* a) {
+  return GatedFfn{a->expert_offsets, a->E, a->d_model, a->d_ff, a->act, a->rows_max,
+                  a->capacity_hint, a->x_packed, a->w_gate, a->b_gate, a->w_up, a->b_up, a->w_down,
+                  a->b_down};
+}
+
+// Plane 1 of the saved tensors.
+void* saved_plane(const void* saved, const moe_gated_ffn_args* a) {
+  return (uint8_t*)saved + (size_t)a->rows_max * a->d_ff * esize(a->dtype);
+}
+
+struct GatedBackwardWs {
+  void *dg, *du;   // [rows_max, d_ff] in dtype
+  float* partial;  // bias gradients
+};
+GatedBackwardWs carve_gated_backward(Carve& c, const moe_gated_ffn_args* a) {
+  GatedBackwardWs w;
+  const size_t n = (size_t)a->rows_max * a->d_ff * esize(a->dtype);
+  w.dg = c.take<uint8_t>(n);
+  w.du = c.take<uint8_t>(n);
+  w.partial = c.take<float>((size_t)gated_bias_grad_partials(a->E, a->d_model, a->d_ff, a->rows_max));
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_gated_ffn_workspace_bytes(size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARGUMENT;
+  *bytes = kAlign;
+  return MOE_OK;
+}
+
+moe_status moe_gated_ffn(const moe_gated_ffn_args* args, void* h_packed, void* y_packed,
+                         void* saved, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  if (!args) return MOE_ERR_INVALID_ARGUMENT;
+  moe_status st = check_gated(args);
+  if (st == MOE_OK) st = check_gated_pointers(args, ws);
+  if (st != MOE_OK) return st;
+  if (args->rows_max > 0 && (!h_packed || !y_packed)) return MOE_ERR_INVALID_ARGUMENT;
+  void* saved_q = saved ? saved_plane(saved, args) : nullptr;
+  if (!aligned16(h_packed) || !aligned16(y_packed) || !aligned16(saved)) return MOE_ERR_MISALIGNED;
+  if (ws_bytes < kAlign) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (fault_injected("moe_gated_ffn")) return MOE_ERR_CUDA;
+  g_launches = 0;
+  if (args->rows_max == 0) return MOE_OK;
+  const GatedFfn g = gated_of(args);
+  int* status = (int*)ws;
+  cudaError_t e;
+  if (args->dtype == MOE_BF16) {
+    e = enqueue_gated_up_bf16(g, h_packed, saved, saved_q, status, stream);
+    if (e == cudaSuccess)
+      e = enqueue_gated_down_bf16(g, h_packed, y_packed, args->out_dtype == MOE_BF16, status, stream);
+  } else {
+    e = enqueue_gated_up_f32(g, (float*)h_packed, (float*)saved, (float*)saved_q, status, stream);
+    if (e == cudaSuccess)
+      e = enqueue_gated_down_f32(g, (const float*)h_packed, (float*)y_packed, status, stream);
+  }
+  return cuda_status(e);
+}
+
+moe_status moe_gated_ffn_backward_workspace_bytes(const moe_gated_ffn_args* args, size_t* bytes) {
+  if (!args || !bytes) return MOE_ERR_INVALID_ARGUMENT;
+  const moe_status st = check_gated(args);
+  if (st != MOE_OK) return st;
+  Carve c{nullptr};
+  carve_gated_backward(c, args);
+  *bytes = c.off;
+  return MOE_OK;
+}
+
+moe_status moe_gated_ffn_backward(const moe_gated_ffn_args* args, const void* dy_packed,
+                                  const void* h_packed, const void* saved,
+                                  const moe_gated_ffn_grads* grads, void* ws, size_t ws_bytes,
+                                  moe_stream_t stream) {
+  if (!args || !grads) return MOE_ERR_INVALID_ARGUMENT;
+  moe_status st = check_gated(args);
+  if (st == MOE_OK) st = check_gated_pointers(args, ws);
+  if (st != MOE_OK) return st;
+  const moe_gated_ffn_grads& o = *grads;
+  if (!valid_dtype(o.dx_dtype) || !valid_dtype(o.grad_dtype)) return MOE_ERR_INVALID_ARGUMENT;
+  if (args->dtype == MOE_F32 && (o.dx_dtype != MOE_F32 || o.grad_dtype != MOE_F32))
+    return MOE_ERR_UNSUPPORTED;
+  if (!o.dw_gate || !o.dw_up || !o.dw_down) return MOE_ERR_INVALID_ARGUMENT;
+  if (args->rows_max > 0 && (!dy_packed || !h_packed || !saved || !o.dx_packed))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned16(dy_packed) || !aligned16(h_packed) || !aligned16(saved) ||
+      !aligned16(o.dx_packed) || !aligned16(o.dw_gate) || !aligned16(o.dw_up) ||
+      !aligned16(o.dw_down) || !aligned16(o.db_gate) || !aligned16(o.db_up) ||
+      !aligned16(o.db_down))
+    return MOE_ERR_MISALIGNED;
+  Carve c{(uint8_t*)ws};
+  const GatedBackwardWs w = carve_gated_backward(c, args);
+  if (ws_bytes < c.off) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (fault_injected("moe_gated_ffn_backward")) return MOE_ERR_CUDA;
+  g_launches = 0;
+  const bool bf16 = args->dtype == MOE_BF16, grad16 = o.grad_dtype == MOE_BF16;
+  const size_t d = args->d_model, f = args->d_ff, E = args->E;
+  if (args->rows_max == 0) {  // no rows: every parameter gradient is zero
+    const std::pair<void*, size_t> zero[] = {{o.dw_gate, E * f * d}, {o.dw_up, E * f * d},
+                                             {o.dw_down, E * d * f}, {o.db_gate, E * f},
+                                             {o.db_up, E * f},       {o.db_down, E * d}};
+    for (const auto& z : zero)
+      if (z.first != nullptr &&
+          cudaMemsetAsync(z.first, 0, z.second * esize(o.grad_dtype), stream) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  const GatedFfn g = gated_of(args);
+  int* status = (int*)ws;
+  const void* saved_q = saved_plane(saved, args);
+  cudaError_t e;
+  if (bf16) {
+    e = enqueue_gated_hidden_grad_bf16(g, dy_packed, saved, saved_q, w.dg, w.du, status, stream);
+    if (e == cudaSuccess)
+      e = enqueue_gated_input_grad_bf16(g, w.dg, w.du, o.dx_packed, o.dx_dtype == MOE_BF16, status,
+                                        stream);
+    if (e == cudaSuccess)
+      e = enqueue_gated_weight_grad_bf16(g, dy_packed, h_packed, w.dg, w.du, o.dw_down, o.dw_gate,
+                                         o.dw_up, grad16, status, stream);
+  } else {
+    const float *dy = (const float*)dy_packed, *h = (const float*)h_packed;
+    float *dg = (float*)w.dg, *du = (float*)w.du;
+    e = enqueue_gated_hidden_grad_f32(g, dy, (const float*)saved, (const float*)saved_q, dg, du,
+                                      status, stream);
+    if (e == cudaSuccess)
+      e = enqueue_gated_input_grad_f32(g, dg, du, (float*)o.dx_packed, status, stream);
+    if (e == cudaSuccess)
+      e = enqueue_gated_weight_grad_f32(g, dy, h, dg, du, (float*)o.dw_down, (float*)o.dw_gate,
+                                        (float*)o.dw_up, status, stream);
+  }
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  GatedBiasGrad b{{dy_packed, w.dg, w.du},
+                  {o.db_down, o.db_gate, o.db_up},
+                  {args->d_model, args->d_ff, args->d_ff}};
+  return cuda_status(enqueue_gated_bias_grad(b, bf16, grad16, args->expert_offsets, args->E,
+                                             args->rows_max, w.partial, stream));
+}
+
+// ---------------------------------------------------------------- gradient norm and clipping
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kMaxGradElems = (int64_t)1 << 43;
+
+// The list in the kernels' form; out is looked at when clipping only.
+moe_status grad_list(const moe_grad_tensor* tensors, int64_t n, bool clip,
+                     std::vector<GradTensor>* list) {
+  if (n < 0 || (n > 0 && !tensors)) return MOE_ERR_INVALID_ARGUMENT;
+  list->reserve((size_t)n);
+  for (int64_t i = 0; i < n; ++i) {
+    const moe_grad_tensor& t = tensors[i];
+    if (!valid_dtype(t.dtype) || t.n < 0 || (t.n > 0 && !t.grad)) return MOE_ERR_INVALID_ARGUMENT;
+    if (t.n >= kMaxGradElems) return MOE_ERR_UNSUPPORTED;
+    if ((uintptr_t)t.grad % esize(t.dtype) != 0) return MOE_ERR_MISALIGNED;
+    if (clip) {
+      if (!valid_dtype(t.out_dtype) || (t.n > 0 && !t.out)) return MOE_ERR_INVALID_ARGUMENT;
+      if ((uintptr_t)t.out % esize(t.out_dtype) != 0) return MOE_ERR_MISALIGNED;
+    }
+    list->push_back(GradTensor{t.grad, t.out, t.n, t.dtype == MOE_BF16 ? 1 : 0,
+                               clip && t.out_dtype == MOE_BF16 ? 1 : 0});
+  }
+  return MOE_OK;
+}
+
+// Whether an output overlaps another output, a gradient other than its own in place, or the norm.
+bool grad_overlap(const std::vector<GradTensor>& list, const float* norm) {
+  struct Span {
+    uintptr_t a, b;
+    bool out;
+  };
+  std::vector<Span> spans;
+  spans.reserve(2 * list.size() + 1);
+  spans.push_back({(uintptr_t)norm, (uintptr_t)norm + 4, false});
+  for (const GradTensor& t : list) {
+    if (t.n == 0) continue;
+    const uintptr_t in = (uintptr_t)t.in, out = (uintptr_t)t.out;
+    spans.push_back({out, out + (size_t)t.n * (t.out_bf16 ? 2 : 4), true});
+    if (in != out || t.in_bf16 != t.out_bf16)
+      spans.push_back({in, in + (size_t)t.n * (t.in_bf16 ? 2 : 4), false});
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span& x, const Span& y) { return x.a < y.a; });
+  uintptr_t end_out = 0, end_any = 0;  // furthest ends so far
+  for (const Span& s : spans) {
+    if (s.a < end_out || (s.out && s.a < end_any)) return true;
+    if (s.b > end_any) end_any = s.b;
+    if (s.out && s.b > end_out) end_out = s.b;
+  }
+  return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_grad_norm_workspace_bytes(size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARGUMENT;
+  *bytes = kAlign + align_up((1 + kGradNormMaxBlocks) * sizeof(double));
+  return MOE_OK;
+}
+
+moe_status moe_grad_norm(const moe_grad_tensor* tensors, int64_t n_tensors, float* norm, void* ws,
+                         size_t ws_bytes, moe_stream_t stream) try {
+  std::vector<GradTensor> list;
+  const moe_status st = grad_list(tensors, n_tensors, false, &list);
+  if (st != MOE_OK) return st;
+  if (!norm || !ws) return MOE_ERR_INVALID_ARGUMENT;
+  if ((uintptr_t)norm % 4 != 0 || ((uintptr_t)ws % kAlign) != 0) return MOE_ERR_MISALIGNED;
+  size_t need = 0;
+  moe_grad_norm_workspace_bytes(&need);
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (fault_injected("moe_grad_norm")) return MOE_ERR_CUDA;
+  g_launches = 0;
+  // the ticket lives in the status block, which the caller zeroed: word 1, after the status word
+  return cuda_status(enqueue_grad_norm(list.data(), n_tensors, (double*)((uint8_t*)ws + kAlign),
+                                       (unsigned*)ws + 1, norm, stream));
+} catch (...) {  // out of host memory
+  return MOE_ERR_CUDA;
+}
+
+moe_status moe_clip_grads(const moe_grad_tensor* tensors, int64_t n_tensors, const float* norm,
+                          float max_norm, moe_stream_t stream) try {
+  std::vector<GradTensor> list;
+  const moe_status st = grad_list(tensors, n_tensors, true, &list);
+  if (st != MOE_OK) return st;
+  if (!norm || !std::isfinite(max_norm) || max_norm < 0) return MOE_ERR_INVALID_ARGUMENT;
+  if ((uintptr_t)norm % 4 != 0) return MOE_ERR_MISALIGNED;
+  if (grad_overlap(list, norm)) return MOE_ERR_INVALID_ARGUMENT;
+  if (fault_injected("moe_clip_grads")) return MOE_ERR_CUDA;
+  g_launches = 0;
+  return cuda_status(enqueue_grad_scale(list.data(), n_tensors, norm, max_norm, stream));
+} catch (...) {
+  return MOE_ERR_CUDA;
 }
 
 moe_status moe_workspace_reset(void* ws, size_t ws_bytes, moe_stream_t stream) {

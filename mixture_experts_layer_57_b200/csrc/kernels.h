@@ -355,4 +355,68 @@ struct SimtGemm {
 // m_extent: the largest M over the experts (grid rows).
 cudaError_t enqueue_simt_gemm(const SimtGemm& p, int64_t m_extent, cudaStream_t stream);
 
+// ---------------------------------------------------------------- gated expert FFN
+// h = act(Wg[e] x + bg[e]) * (Wu[e] x + bu[e]), y = Wd[e] h + bd[e] on expert-major rows, and its
+// backward pass (f32: fp32 FMA kernels; bf16: tcgen05 kernels). saved_a = act(zg) and saved_q =
+// zu act'(zg) are what the backward pass needs of the pre-activations (NULL: not kept).
+struct GatedFfn {
+  const int32_t* offsets;
+  int E, d, f, act;
+  int64_t rows_max, capacity_hint;
+  const void *x, *w_gate, *b_gate, *w_up, *b_up, *w_down, *b_down;
+};
+cudaError_t enqueue_gated_up_f32(const GatedFfn& g, float* h, float* saved_a, float* saved_q,
+                                 int* status, cudaStream_t stream);
+cudaError_t enqueue_gated_down_f32(const GatedFfn& g, const float* h, float* y, int* status,
+                                   cudaStream_t stream);
+cudaError_t enqueue_gated_hidden_grad_f32(const GatedFfn& g, const float* dy, const float* saved_a,
+                                          const float* saved_q, float* dg, float* du, int* status,
+                                          cudaStream_t stream);
+cudaError_t enqueue_gated_input_grad_f32(const GatedFfn& g, const float* dg, const float* du,
+                                         float* dx, int* status, cudaStream_t stream);
+cudaError_t enqueue_gated_weight_grad_f32(const GatedFfn& g, const float* dy, const float* h,
+                                          const float* dg, const float* du, float* dw_down,
+                                          float* dw_gate, float* dw_up, int* status,
+                                          cudaStream_t stream);
+cudaError_t enqueue_gated_up_bf16(const GatedFfn& g, void* h, void* saved_a, void* saved_q,
+                                  int* status, cudaStream_t stream);
+cudaError_t enqueue_gated_down_bf16(const GatedFfn& g, const void* h, void* y, bool y_bf16,
+                                    int* status, cudaStream_t stream);
+cudaError_t enqueue_gated_hidden_grad_bf16(const GatedFfn& g, const void* dy, const void* saved_a,
+                                           const void* saved_q, void* dg, void* du, int* status,
+                                           cudaStream_t stream);
+cudaError_t enqueue_gated_input_grad_bf16(const GatedFfn& g, const void* dg, const void* du,
+                                          void* dx, bool dx_bf16, int* status, cudaStream_t stream);
+// The three weight gradients in one launch, fp32 or bf16.
+cudaError_t enqueue_gated_weight_grad_bf16(const GatedFfn& g, const void* dy, const void* h,
+                                           const void* dg, const void* du, void* dw_down,
+                                           void* dw_gate, void* dw_up, bool grad_bf16, int* status,
+                                           cudaStream_t stream);
+// Bias gradients: column sums of up to three matrices over each segment's rows, in one launch
+// (and a second one that adds the row splits). Any out may be NULL.
+struct GatedBiasGrad {
+  const void* src[3];  // [rows_max, n[i]] in the layer's type
+  void* out[3];        // [E, n[i]]
+  int n[3];
+};
+int64_t gated_bias_grad_partials(int E, int d, int f, int64_t rows_max);  // floats of scratch
+cudaError_t enqueue_gated_bias_grad(const GatedBiasGrad& b, bool bf16, bool out_bf16,
+                                    const int32_t* offsets, int E, int64_t rows_max,
+                                    float* partial, cudaStream_t stream);
+
+// ---------------------------------------------------------------- gradient norm and clipping
+// One tensor of a gradient list.
+struct GradTensor {
+  const void* in;
+  void* out;          // clipping only
+  int64_t n;
+  int in_bf16, out_bf16;
+};
+constexpr int kGradNormMaxBlocks = 2048;
+// partials: 1 + kGradNormMaxBlocks doubles of scratch; *ticket is zero before and after.
+cudaError_t enqueue_grad_norm(const GradTensor* t, int64_t n_tensors, double* partials,
+                              unsigned* ticket, float* norm, cudaStream_t stream);
+cudaError_t enqueue_grad_scale(const GradTensor* t, int64_t n_tensors, const float* norm,
+                               float max_norm, cudaStream_t stream);
+
 }  // namespace moe

@@ -21,6 +21,8 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "moe.h")
 MOE_F32, MOE_BF16 = 0, 1
 MOE_EPILOGUE_BIAS_GELU, MOE_EPILOGUE_BIAS = 0, 1
 MOE_OVERFLOW_FIRST_COME, MOE_OVERFLOW_PRIORITY = 0, 1
+MOE_GATE_SILU, MOE_GATE_GELU = 0, 1
+GATE_ACTS = {"silu": MOE_GATE_SILU, "gelu": MOE_GATE_GELU}
 STATUS_BLOCK_BYTES = 256
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARGUMENT", 2: "MOE_ERR_UNSUPPORTED",
                 3: "MOE_ERR_WORKSPACE_TOO_SMALL", 4: "MOE_ERR_CUDA", 5: "MOE_ERR_DEVICE_FLAG",
@@ -60,6 +62,27 @@ class LayerGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "dx", "dw_router", "db_router", "dw1", "db1", "dw2", "db2", "dense_dw1", "dense_db1",
         "dense_dw2", "dense_db2", "dgates", "dlogits")]
+
+
+class GatedFfnArgs(ctypes.Structure):
+    _fields_ = [("x_packed", ctypes.c_void_p), ("expert_offsets", ctypes.c_void_p),
+                ("E", ctypes.c_int), ("rows_max", ctypes.c_int64), ("d_model", ctypes.c_int),
+                ("d_ff", ctypes.c_int), ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("act", ctypes.c_int), ("w_gate", ctypes.c_void_p), ("b_gate", ctypes.c_void_p),
+                ("w_up", ctypes.c_void_p), ("b_up", ctypes.c_void_p),
+                ("w_down", ctypes.c_void_p), ("b_down", ctypes.c_void_p),
+                ("capacity_hint", ctypes.c_int64)]
+
+
+class GatedFfnGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "dx_packed", "dw_gate", "dw_up", "dw_down", "db_gate", "db_up", "db_down")] + [
+        ("dx_dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int)]
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int)]
 
 
 _lib = None
@@ -110,6 +133,14 @@ def lib() -> ctypes.CDLL:
             "moe_layer_train_workspace_bytes": ([P(LayerArgs), P(sz)], i32),
             "moe_layer_forward_train": ([P(LayerArgs), vp, P(LayerAux), vp, sz, vp], i32),
             "moe_layer_backward": ([P(LayerArgs), vp, f32, f32, P(LayerGrads), vp, sz, vp], i32),
+            "moe_gated_ffn_workspace_bytes": ([P(sz)], i32),
+            "moe_gated_ffn": ([P(GatedFfnArgs), vp, vp, vp, vp, sz, vp], i32),
+            "moe_gated_ffn_backward_workspace_bytes": ([P(GatedFfnArgs), P(sz)], i32),
+            "moe_gated_ffn_backward": ([P(GatedFfnArgs), vp, vp, vp, P(GatedFfnGrads), vp, sz, vp],
+                                       i32),
+            "moe_grad_norm_workspace_bytes": ([P(sz)], i32),
+            "moe_grad_norm": ([vp, i64, vp, vp, sz, vp], i32),
+            "moe_clip_grads": ([vp, i64, vp, f32, vp], i32),
             "moe_workspace_reset": ([vp, sz, vp], i32),
             "moe_get_device_error": ([vp, P(i32), vp], i32),
             "moe_selftest_bounded_wait": ([vp, sz, ctypes.c_uint64, vp], i32),
@@ -555,6 +586,206 @@ def moe_layer_backward(args: LayerArgs, d_out: torch.Tensor, grads: dict, ws: to
         ctypes.byref(args), _ptr(d_out), aux_weight, z_weight, ctypes.byref(g), _ptr(ws),
         ws.numel(), _stream(stream)))
     return grads
+
+
+# ---------------------------------------------------------------- gated expert FFN
+
+def _stream_of(t: torch.Tensor, stream):
+    return torch.cuda.current_stream(t.device) if stream is None else stream
+
+
+def _expect(name: str, t: torch.Tensor, like: torch.Tensor, shape: tuple, dtype=None):
+    if t.device != like.device or t.dtype != (dtype or like.dtype) or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected {shape} {dtype or like.dtype} on {like.device}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def gated_ffn_args(x_packed: torch.Tensor, expert_offsets: torch.Tensor, w_gate: torch.Tensor,
+                   w_up: torch.Tensor, w_down: torch.Tensor, b_gate=None, b_up=None, b_down=None,
+                   act: str = "silu", out_dtype=None, rows_max=None,
+                   capacity_hint=None) -> GatedFfnArgs:
+    """A ``moe_gated_ffn_args`` struct from tensors, which it keeps alive. ``act`` is "silu" or
+    "gelu"; ``out_dtype`` the type of y (default fp32, as moe_combine reads it)."""
+    if act not in GATE_ACTS:
+        raise ValueError(f"act must be one of {sorted(GATE_ACTS)}, got {act!r}")
+    dt = _dt(x_packed)
+    E, d_ff, d = w_gate.shape
+    if x_packed.dim() != 2:
+        raise ValueError("x_packed must be [rows, d_model]")
+    if rows_max is None:
+        rows_max = x_packed.shape[0]
+    if not 0 <= rows_max <= x_packed.shape[0]:
+        raise ValueError(f"rows_max {rows_max} is outside [0, {x_packed.shape[0]}]")
+    _expect("x_packed", x_packed, x_packed, (x_packed.shape[0], d))
+    _expect("expert_offsets", expert_offsets, x_packed, (E + 1,), torch.int32)
+    for name, t, shape in (("w_gate", w_gate, (E, d_ff, d)), ("w_up", w_up, (E, d_ff, d)),
+                           ("w_down", w_down, (E, d, d_ff)), ("b_gate", b_gate, (E, d_ff)),
+                           ("b_up", b_up, (E, d_ff)), ("b_down", b_down, (E, d))):
+        if t is not None:
+            _expect(name, t, x_packed, shape)
+    out = torch.float32 if out_dtype is None else out_dtype
+    if out not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"unsupported out_dtype {out}")
+    a = GatedFfnArgs(_ptr(x_packed), _ptr(expert_offsets), E, rows_max, d, d_ff, dt,
+                     MOE_BF16 if out == torch.bfloat16 else MOE_F32, GATE_ACTS[act], _ptr(w_gate),
+                     _ptr(b_gate), _ptr(w_up), _ptr(b_up), _ptr(w_down), _ptr(b_down),
+                     rows_max if capacity_hint is None else capacity_hint)
+    a.tensors = (x_packed, expert_offsets, w_gate, w_up, w_down, b_gate, b_up, b_down)
+    return a
+
+
+def moe_gated_ffn_workspace_bytes() -> int:
+    return _ws_bytes("moe_gated_ffn_workspace_bytes")
+
+
+def moe_gated_ffn_backward_workspace_bytes(args: GatedFfnArgs) -> int:
+    return _ws_bytes("moe_gated_ffn_backward_workspace_bytes", ctypes.byref(args))
+
+
+def moe_gated_ffn(args: GatedFfnArgs, y_packed=None, h_packed=None, saved=None, train: bool = False,
+                  ws=None, stream=None) -> dict:
+    """The gated expert FFN forward. ``saved`` ([2, rows, d_ff] in x's type, or ``train=True`` to
+    allocate it) keeps what moe_gated_ffn_backward needs besides ``h_packed``."""
+    x = args.tensors[0]
+    out_dtype = _torch_dt(args.out_dtype)
+    rows, d, d_ff = max(args.rows_max, 1), args.d_model, args.d_ff
+    with torch.cuda.device(x.device):
+        s = _stream_of(x, stream)
+        with torch.cuda.stream(s):  # new tensors belong to the stream that writes them
+            if h_packed is None:
+                h_packed = torch.empty(rows, d_ff, dtype=x.dtype, device=x.device)
+            if y_packed is None:
+                y_packed = torch.empty(rows, d, dtype=out_dtype, device=x.device)
+            if saved is None and train:
+                saved = torch.empty(2, args.rows_max, d_ff, dtype=x.dtype, device=x.device)
+            if ws is None:
+                ws = workspace(moe_gated_ffn_workspace_bytes(), x.device)
+        for name, t, cols, dtype in (("h_packed", h_packed, d_ff, x.dtype),
+                                     ("y_packed", y_packed, d, out_dtype)):
+            if t.dim() != 2 or t.shape[0] < args.rows_max:
+                raise ValueError(f"{name} must be [at least {args.rows_max}, {cols}]")
+            _expect(name, t, x, (t.shape[0], cols), dtype)
+        if saved is not None:
+            _expect("saved", saved, x, (2, args.rows_max, d_ff))
+        _check("moe_gated_ffn", lib().moe_gated_ffn(
+            ctypes.byref(args), _ptr(h_packed), _ptr(y_packed), _ptr(saved), _ptr(ws), ws.numel(),
+            _stream(s)))
+    return dict(y_packed=y_packed, h_packed=h_packed, saved=saved, ws=ws)
+
+
+def moe_gated_ffn_backward(args: GatedFfnArgs, dy_packed: torch.Tensor, h_packed: torch.Tensor,
+                           saved: torch.Tensor, grads: Optional[dict] = None, dx_dtype=None,
+                           grad_dtype=None, ws=None, stream=None) -> dict:
+    """Gradients of moe_gated_ffn: fills ``grads`` (dx_packed, dw_gate, dw_up, dw_down and, for the
+    biases that args has, db_gate, db_up, db_down); what is missing there is allocated, dx in
+    ``dx_dtype`` and the parameters' in ``grad_dtype`` (default fp32, as the layer's backward)."""
+    x, _, w_gate, w_up, w_down, b_gate, b_up, b_down = args.tensors
+    grads = {} if grads is None else grads
+    like = dict(dw_gate=w_gate, dw_up=w_up, dw_down=w_down, db_gate=b_gate, db_up=b_up,
+                db_down=b_down)
+    like = {n: t for n, t in like.items() if t is not None}
+    unknown = set(grads) - set(like) - {"dx_packed"}
+    if unknown:
+        raise ValueError(f"no such gradients: {sorted(unknown)}")
+    given = [t for n, t in grads.items() if n != "dx_packed" and t is not None]
+    if grad_dtype is None:
+        grad_dtype = given[0].dtype if given else torch.float32
+    if dx_dtype is None:
+        dx_dtype = grads["dx_packed"].dtype if grads.get("dx_packed") is not None else x.dtype
+    with torch.cuda.device(x.device):
+        s = _stream_of(x, stream)
+        with torch.cuda.stream(s):
+            if grads.get("dx_packed") is None:
+                grads["dx_packed"] = torch.empty(max(args.rows_max, 1), args.d_model,
+                                                 dtype=dx_dtype, device=x.device)
+            for n, t in like.items():
+                if grads.get(n) is None:
+                    grads[n] = torch.empty(t.shape, dtype=grad_dtype, device=x.device)
+            if ws is None:
+                ws = workspace(moe_gated_ffn_backward_workspace_bytes(args), x.device)
+        for name, t, cols, dtype in (("dy_packed", dy_packed, args.d_model, x.dtype),
+                                     ("h_packed", h_packed, args.d_ff, x.dtype),
+                                     ("dx_packed", grads["dx_packed"], args.d_model, dx_dtype)):
+            if t.dim() != 2 or t.shape[0] < args.rows_max:
+                raise ValueError(f"{name} must be [at least {args.rows_max}, {cols}]")
+            _expect(name, t, x, (t.shape[0], cols), dtype)
+        _expect("saved", saved, x, (2, args.rows_max, args.d_ff))
+        for n, t in like.items():
+            _expect(n, grads[n], x, tuple(t.shape), grad_dtype)
+        g = GatedFfnGrads(**{n: _ptr(t) for n, t in grads.items()}, dx_dtype=_dt(grads["dx_packed"]),
+                          grad_dtype=_dt(grads["dw_gate"]))
+        _check("moe_gated_ffn_backward", lib().moe_gated_ffn_backward(
+            ctypes.byref(args), _ptr(dy_packed), _ptr(h_packed), _ptr(saved), ctypes.byref(g),
+            _ptr(ws), ws.numel(), _stream(s)))
+    return grads
+
+
+# ---------------------------------------------------------------- gradient norm and clipping
+
+def _grad_list(grads, out=None):
+    """The tensors as a ``moe_grad_tensor`` array, and their device."""
+    if not grads:
+        raise ValueError("the list of gradients is empty")
+    outs = grads if out is None else out
+    if len(outs) != len(grads):
+        raise ValueError(f"{len(grads)} gradients and {len(outs)} outputs")
+    dev = grads[0].device
+    rows = []
+    for g, o in zip(grads, outs):
+        if g.device != dev or o.device != dev:
+            raise ValueError("gradients and outputs must be on one device")
+        if o is not g and o.numel() != g.numel():
+            raise ValueError(f"an output of {o.numel()} elements for a gradient of {g.numel()}")
+        rows.append((_ptr(g), _ptr(o), g.numel(), _dt(g), _dt(o)))
+    return (GradTensor * len(rows))(*rows), len(rows), dev
+
+
+def moe_grad_norm_workspace_bytes() -> int:
+    return _ws_bytes("moe_grad_norm_workspace_bytes")
+
+
+def _grad_norm(table, n, dev, norm, ws, s):
+    with torch.cuda.stream(s):
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = workspace(moe_grad_norm_workspace_bytes(), dev)
+    if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != dev:
+        raise ValueError("norm must be one fp32 value on the gradients' device")
+    _check("moe_grad_norm", lib().moe_grad_norm(table, n, _ptr(norm), _ptr(ws), ws.numel(),
+                                                _stream(s)))
+    return norm
+
+
+def moe_grad_norm(grads, norm=None, ws=None, stream=None) -> torch.Tensor:
+    """The 2-norm of all elements of a list of tensors (fp32 or bf16), as one fp32 value on the
+    device."""
+    table, n, dev = _grad_list(grads)
+    with torch.cuda.device(dev):
+        return _grad_norm(table, n, dev, norm, ws, _stream_of(grads[0], stream))
+
+
+def moe_clip_grads(grads, norm: torch.Tensor, max_norm: float, out=None, stream=None):
+    """``out`` (default: in place) = grads * min(1, max_norm / (norm + 1e-6)), with ``norm`` one
+    fp32 value on the device."""
+    table, n, dev = _grad_list(grads, out)
+    if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != dev:
+        raise ValueError("norm must be one fp32 value on the gradients' device")
+    with torch.cuda.device(dev):
+        _check("moe_clip_grads", lib().moe_clip_grads(table, n, _ptr(norm), max_norm,
+                                                      _stream(_stream_of(grads[0], stream))))
+    return grads if out is None else out
+
+
+def moe_clip_grad_norm(grads, max_norm: float, out=None, norm=None, ws=None,
+                       stream=None) -> torch.Tensor:
+    """moe_grad_norm, then moe_clip_grads by it; returns the norm before clipping."""
+    table, n, dev = _grad_list(grads, out)
+    with torch.cuda.device(dev):
+        s = _stream_of(grads[0], stream)
+        norm = _grad_norm(table, n, dev, norm, ws, s)
+        _check("moe_clip_grads", lib().moe_clip_grads(table, n, _ptr(norm), max_norm, _stream(s)))
+    return norm
 
 
 def moe_workspace_reset(ws: torch.Tensor, stream=None):
