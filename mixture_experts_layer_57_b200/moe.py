@@ -8,6 +8,8 @@ present the calls raise.
 """
 from __future__ import annotations
 
+import array
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -590,13 +592,23 @@ def moe_layer_backward(args: LayerArgs, d_out: torch.Tensor, grads: dict, ws: to
 
 # ---------------------------------------------------------------- gated expert FFN
 
-def _stream_of(t: torch.Tensor, stream):
-    return torch.cuda.current_stream(t.device) if stream is None else stream
+def _launch_on(dev: torch.device, stream):
+    """Where a call runs: the stream (default: the device's current one), and a context in which
+    that device is current and new tensors belong to that stream."""
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if s.device != dev:
+        raise ValueError(f"a stream of {s.device} for tensors on {dev}")
+    if stream is None and dev.index == torch.cuda.current_device():
+        return s, contextlib.nullcontext()  # as it is already
+    ctx = contextlib.ExitStack()
+    ctx.enter_context(torch.cuda.device(dev))
+    ctx.enter_context(torch.cuda.stream(s))
+    return s, ctx
 
 
 def _expect(name: str, t: torch.Tensor, like: torch.Tensor, shape: tuple, dtype=None):
-    if t.device != like.device or t.dtype != (dtype or like.dtype) or tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected {shape} {dtype or like.dtype} on {like.device}, got "
+    if t.shape != shape or t.dtype != (dtype or like.dtype) or t.device != like.device:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype or like.dtype} on {like.device}, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
 
 
@@ -642,34 +654,38 @@ def moe_gated_ffn_backward_workspace_bytes(args: GatedFfnArgs) -> int:
     return _ws_bytes("moe_gated_ffn_backward_workspace_bytes", ctypes.byref(args))
 
 
+def _rows_of(name: str, t: torch.Tensor, x: torch.Tensor, rows: int, cols: int, dtype):
+    if t.dim() != 2 or t.shape[0] < rows:
+        raise ValueError(f"{name} must be [at least {rows}, {cols}]")
+    _expect(name, t, x, (t.shape[0], cols), dtype)
+
+
 def moe_gated_ffn(args: GatedFfnArgs, y_packed=None, h_packed=None, saved=None, train: bool = False,
                   ws=None, stream=None) -> dict:
     """The gated expert FFN forward. ``saved`` ([2, rows, d_ff] in x's type, or ``train=True`` to
     allocate it) keeps what moe_gated_ffn_backward needs besides ``h_packed``."""
     x = args.tensors[0]
-    out_dtype = _torch_dt(args.out_dtype)
-    rows, d, d_ff = max(args.rows_max, 1), args.d_model, args.d_ff
-    with torch.cuda.device(x.device):
-        s = _stream_of(x, stream)
-        with torch.cuda.stream(s):  # new tensors belong to the stream that writes them
-            if h_packed is None:
-                h_packed = torch.empty(rows, d_ff, dtype=x.dtype, device=x.device)
-            if y_packed is None:
-                y_packed = torch.empty(rows, d, dtype=out_dtype, device=x.device)
-            if saved is None and train:
-                saved = torch.empty(2, args.rows_max, d_ff, dtype=x.dtype, device=x.device)
-            if ws is None:
-                ws = workspace(moe_gated_ffn_workspace_bytes(), x.device)
-        for name, t, cols, dtype in (("h_packed", h_packed, d_ff, x.dtype),
-                                     ("y_packed", y_packed, d, out_dtype)):
-            if t.dim() != 2 or t.shape[0] < args.rows_max:
-                raise ValueError(f"{name} must be [at least {args.rows_max}, {cols}]")
-            _expect(name, t, x, (t.shape[0], cols), dtype)
+    dev, dtype, out_dtype = x.device, x.dtype, _torch_dt(args.out_dtype)
+    rows, d, d_ff = args.rows_max, args.d_model, args.d_ff
+    s, ctx = _launch_on(dev, stream)
+    with ctx:
+        if h_packed is None:
+            h_packed = torch.empty(max(rows, 1), d_ff, dtype=dtype, device=dev)
+        else:
+            _rows_of("h_packed", h_packed, x, rows, d_ff, dtype)
+        if y_packed is None:
+            y_packed = torch.empty(max(rows, 1), d, dtype=out_dtype, device=dev)
+        else:
+            _rows_of("y_packed", y_packed, x, rows, d, out_dtype)
         if saved is not None:
-            _expect("saved", saved, x, (2, args.rows_max, d_ff))
+            _expect("saved", saved, x, (2, rows, d_ff))
+        elif train:
+            saved = torch.empty(2, rows, d_ff, dtype=dtype, device=dev)
+        if ws is None:
+            ws = workspace(moe_gated_ffn_workspace_bytes(), dev)
         _check("moe_gated_ffn", lib().moe_gated_ffn(
             ctypes.byref(args), _ptr(h_packed), _ptr(y_packed), _ptr(saved), _ptr(ws), ws.numel(),
-            _stream(s)))
+            s.cuda_stream))
     return dict(y_packed=y_packed, h_packed=h_packed, saved=saved, ws=ws)
 
 
@@ -692,68 +708,84 @@ def moe_gated_ffn_backward(args: GatedFfnArgs, dy_packed: torch.Tensor, h_packed
         grad_dtype = given[0].dtype if given else torch.float32
     if dx_dtype is None:
         dx_dtype = grads["dx_packed"].dtype if grads.get("dx_packed") is not None else x.dtype
-    with torch.cuda.device(x.device):
-        s = _stream_of(x, stream)
-        with torch.cuda.stream(s):
-            if grads.get("dx_packed") is None:
-                grads["dx_packed"] = torch.empty(max(args.rows_max, 1), args.d_model,
-                                                 dtype=dx_dtype, device=x.device)
-            for n, t in like.items():
-                if grads.get(n) is None:
-                    grads[n] = torch.empty(t.shape, dtype=grad_dtype, device=x.device)
-            if ws is None:
-                ws = workspace(moe_gated_ffn_backward_workspace_bytes(args), x.device)
-        for name, t, cols, dtype in (("dy_packed", dy_packed, args.d_model, x.dtype),
-                                     ("h_packed", h_packed, args.d_ff, x.dtype),
-                                     ("dx_packed", grads["dx_packed"], args.d_model, dx_dtype)):
-            if t.dim() != 2 or t.shape[0] < args.rows_max:
-                raise ValueError(f"{name} must be [at least {args.rows_max}, {cols}]")
-            _expect(name, t, x, (t.shape[0], cols), dtype)
-        _expect("saved", saved, x, (2, args.rows_max, args.d_ff))
+    rows = args.rows_max
+    s, ctx = _launch_on(x.device, stream)
+    with ctx:
+        _rows_of("dy_packed", dy_packed, x, rows, args.d_model, x.dtype)
+        _rows_of("h_packed", h_packed, x, rows, args.d_ff, x.dtype)
+        _expect("saved", saved, x, (2, rows, args.d_ff))
+        if grads.get("dx_packed") is None:
+            grads["dx_packed"] = torch.empty(max(rows, 1), args.d_model, dtype=dx_dtype,
+                                             device=x.device)
+        else:
+            _rows_of("dx_packed", grads["dx_packed"], x, rows, args.d_model, dx_dtype)
         for n, t in like.items():
-            _expect(n, grads[n], x, tuple(t.shape), grad_dtype)
+            if grads.get(n) is None:
+                grads[n] = torch.empty(t.shape, dtype=grad_dtype, device=x.device)
+            else:
+                _expect(n, grads[n], x, t.shape, grad_dtype)
+        if ws is None:
+            ws = workspace(moe_gated_ffn_backward_workspace_bytes(args), x.device)
         g = GatedFfnGrads(**{n: _ptr(t) for n, t in grads.items()}, dx_dtype=_dt(grads["dx_packed"]),
                           grad_dtype=_dt(grads["dw_gate"]))
         _check("moe_gated_ffn_backward", lib().moe_gated_ffn_backward(
             ctypes.byref(args), _ptr(dy_packed), _ptr(h_packed), _ptr(saved), ctypes.byref(g),
-            _ptr(ws), ws.numel(), _stream(s)))
+            _ptr(ws), ws.numel(), s.cuda_stream))
     return grads
 
 
 # ---------------------------------------------------------------- gradient norm and clipping
 
+_GRAD_CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
 def _grad_list(grads, out=None):
-    """The tensors as a ``moe_grad_tensor`` array, and their device."""
+    """The tensors as an array of ``moe_grad_tensor`` (host memory), their number and device."""
     if not grads:
         raise ValueError("the list of gradients is empty")
-    outs = grads if out is None else out
-    if len(outs) != len(grads):
-        raise ValueError(f"{len(grads)} gradients and {len(outs)} outputs")
-    dev = grads[0].device
-    rows = []
-    for g, o in zip(grads, outs):
-        if g.device != dev or o.device != dev:
-            raise ValueError("gradients and outputs must be on one device")
-        if o is not g and o.numel() != g.numel():
-            raise ValueError(f"an output of {o.numel()} elements for a gradient of {g.numel()}")
-        rows.append((_ptr(g), _ptr(o), g.numel(), _dt(g), _dt(o)))
-    return (GradTensor * len(rows))(*rows), len(rows), dev
+    n = len(grads)
+    if out is not None and len(out) != n:
+        raise ValueError(f"{n} gradients and {len(out)} outputs")
+    tensors = [*grads] if out is None else [*grads, *out]
+    # whole-list passes: a step of a small model clips its gradients in some tens of microseconds
+    T = torch.Tensor
+    if len(set(map(T.get_device, tensors))) != 1:
+        raise ValueError("gradients and outputs must be on one device")
+    if not all(map(T.is_contiguous, tensors)):
+        raise ValueError("gradients and outputs must be contiguous")
+    ptrs, sizes = list(map(T.data_ptr, tensors)), list(map(T.numel, tensors))
+    if sizes[:n] != sizes[-n:]:
+        raise ValueError("every output must have its gradient's size")
+    try:
+        codes = [_GRAD_CODES[t.dtype] for t in tensors]
+    except KeyError as e:
+        raise ValueError(f"unsupported dtype {e.args[0]}") from None
+    words = array.array("q", bytes(32 * n))  # four 64-bit words a tensor
+    words[0::4] = array.array("q", ptrs[:n])
+    words[1::4] = array.array("q", ptrs[-n:])
+    words[2::4] = array.array("q", sizes[:n])
+    words[3::4] = array.array("q", [a | b << 32 for a, b in zip(codes, codes[-n:])])
+    return (ctypes.c_int64 * (4 * n)).from_buffer(words), n, grads[0].device
 
 
 def moe_grad_norm_workspace_bytes() -> int:
     return _ws_bytes("moe_grad_norm_workspace_bytes")
 
 
-def _grad_norm(table, n, dev, norm, ws, s):
-    with torch.cuda.stream(s):
-        if norm is None:
-            norm = torch.empty((), dtype=torch.float32, device=dev)
-        if ws is None:
-            ws = workspace(moe_grad_norm_workspace_bytes(), dev)
+def _check_norm(norm: torch.Tensor, dev):
     if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != dev:
         raise ValueError("norm must be one fp32 value on the gradients' device")
-    _check("moe_grad_norm", lib().moe_grad_norm(table, n, _ptr(norm), _ptr(ws), ws.numel(),
-                                                _stream(s)))
+
+
+def _grad_norm(table, n, dev, norm, ws, s):
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+    else:
+        _check_norm(norm, dev)
+    if ws is None:
+        ws = workspace(moe_grad_norm_workspace_bytes(), dev)
+    _check("moe_grad_norm", lib().moe_grad_norm(table, n, norm.data_ptr(), _ptr(ws), ws.numel(),
+                                                s.cuda_stream))
     return norm
 
 
@@ -761,19 +793,20 @@ def moe_grad_norm(grads, norm=None, ws=None, stream=None) -> torch.Tensor:
     """The 2-norm of all elements of a list of tensors (fp32 or bf16), as one fp32 value on the
     device."""
     table, n, dev = _grad_list(grads)
-    with torch.cuda.device(dev):
-        return _grad_norm(table, n, dev, norm, ws, _stream_of(grads[0], stream))
+    s, ctx = _launch_on(dev, stream)
+    with ctx:
+        return _grad_norm(table, n, dev, norm, ws, s)
 
 
 def moe_clip_grads(grads, norm: torch.Tensor, max_norm: float, out=None, stream=None):
     """``out`` (default: in place) = grads * min(1, max_norm / (norm + 1e-6)), with ``norm`` one
     fp32 value on the device."""
     table, n, dev = _grad_list(grads, out)
-    if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != dev:
-        raise ValueError("norm must be one fp32 value on the gradients' device")
-    with torch.cuda.device(dev):
-        _check("moe_clip_grads", lib().moe_clip_grads(table, n, _ptr(norm), max_norm,
-                                                      _stream(_stream_of(grads[0], stream))))
+    _check_norm(norm, dev)
+    s, ctx = _launch_on(dev, stream)
+    with ctx:
+        _check("moe_clip_grads", lib().moe_clip_grads(table, n, norm.data_ptr(), max_norm,
+                                                      s.cuda_stream))
     return grads if out is None else out
 
 
@@ -781,10 +814,11 @@ def moe_clip_grad_norm(grads, max_norm: float, out=None, norm=None, ws=None,
                        stream=None) -> torch.Tensor:
     """moe_grad_norm, then moe_clip_grads by it; returns the norm before clipping."""
     table, n, dev = _grad_list(grads, out)
-    with torch.cuda.device(dev):
-        s = _stream_of(grads[0], stream)
+    s, ctx = _launch_on(dev, stream)
+    with ctx:
         norm = _grad_norm(table, n, dev, norm, ws, s)
-        _check("moe_clip_grads", lib().moe_clip_grads(table, n, _ptr(norm), max_norm, _stream(s)))
+        _check("moe_clip_grads", lib().moe_clip_grads(table, n, norm.data_ptr(), max_norm,
+                                                      s.cuda_stream))
     return norm
 
 

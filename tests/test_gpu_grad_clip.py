@@ -147,3 +147,19 @@ def test_graph_and_stream(cuda_ok):
     torch.cuda.synchronize()
     assert torch.equal(norm, wnorm)
     assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("src", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dst", [torch.float32, torch.bfloat16])
+def test_places_of_any_relative_alignment(cuda_ok, src, dst):
+    # gradient and output start at every distance from a 16-byte boundary, with lengths around the
+    # vectors' and chunks' ends
+    for a in range(8):
+        for b in range(8):
+            sizes = [1 + (5 * a + 3 * b) % 40, 61 + a, 8200 + 7 * b]
+            grads = make([n + a for n in sizes], [src], seed=8 * a + b)
+            grads = [g[a:] for g in grads]
+            space = [torch.full((n + b + 3,), 77.0, dtype=dst, device="cuda") for n in sizes]
+            check(grads, 0.5, out=[s[b:b + n] for s, n in zip(space, sizes)])
+            for s, n in zip(space, sizes):
+                assert bool((s[:b] == 77.0).all()) and bool((s[b + n:] == 77.0).all())
