@@ -414,8 +414,9 @@ moe_status moe_layer_backward(const moe_layer_args* args, const void* d_out, flo
  * b_down: [E, d_model] or NULL; all in dtype. x_packed: [rows_max, d_model] in dtype.
  * h_packed: [rows_max, d_ff] in dtype (bf16 rounds h, the second product's operand).
  * y_packed: [rows_max, d_model] in out_dtype (fp32 layers: MOE_F32 only).
- * saved: NULL, or [2, rows_max, d_ff] in dtype for the backward pass: plane 0 receives act(zg),
- * plane 1 zu act'(zg).
+ * saved: NULL, or [2, rows_max, d_ff] in dtype for the backward pass, which alone reads it: plane 0
+ * receives act(zg), plane 1 zu act'(zg) (bf16 layers: eight neighbours in 16 bits each with one
+ * exponent between them, 11 bits where bf16 would keep 8).
  * Rows outside every segment are neither read nor written. Offsets that are not non-decreasing
  * within [0, rows_max] set MOE_DEVERR_BAD_OFFSETS. capacity_hint: an upper bound on the rows of
  * any one expert (normally C); it selects tile sizes and how sums are split, so it may change

@@ -1,6 +1,8 @@
 // Gate activations of the gated expert FFN and their derivatives.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace moe {
@@ -8,22 +10,102 @@ namespace moe {
 // a = act(z), da = act'(z).
 //   SiLU: act = z s, act' = s (1 + z (1 - s)) with s = 1 / (1 + e^-z)
 //   GeLU (erf form): act = z Phi(z), act' = Phi(z) + z phi(z)
-// e^-z overflowing to infinity gives s = 0, the limit. FAST uses the approximate exponential and
-// division (a few units in the last place of fp32), far below the bf16 rounding that follows.
+// e^-z overflowing to infinity gives s = 0, the limit. FAST (bf16 layers) uses the approximate
+// exponential and division, and Phi from Abramowitz and Stegun, Handbook of Mathematical
+// Functions, 7.1.26 (erf to 1.5e-7, with the exponential that phi needs too): errors near 2^-22,
+// far below the bf16 rounding that follows, in a third of erff's instructions.
 template <bool FAST = false>
 __device__ __forceinline__ void gate_act(float z, int act, float& a, float& da) {
   if (act == MOE_GATE_SILU) {
     const float s = FAST ? __fdividef(1.0f, 1.0f + __expf(-z)) : 1.0f / (1.0f + expf(-z));
     a = z * s;
     da = s * (1.0f + z * (1.0f - s));
+  } else if constexpr (FAST) {
+    const float x = fabsf(z) * 0.70710678118654752440f;
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    const float e = __expf(-x * x);
+    const float poly =
+        t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                 0.254829592f);
+    const float tail = 0.5f * poly * e;  // Phi(-|z|)
+    const float cdf = z >= 0.0f ? 1.0f - tail : tail;
+    a = z * cdf;
+    da = fmaf(z * 0.39894228040143267794f, e, cdf);
   } else {
     const float cdf = 0.5f * (1.0f + erff(z * 0.70710678118654752440f));
     a = z * cdf;
-    da = cdf + z * 0.39894228040143267794f * (FAST ? __expf(-0.5f * z * z) : expf(-0.5f * z * z));
+    da = cdf + z * 0.39894228040143267794f * expf(-0.5f * z * z);
   }
 }
 
-// 3D tiled bulk tensor copy global -> shared, completion counted on `bar` in bytes.
+// Eight values in 8 x 16 bits with one exponent between them (what the forward pass of a bf16
+// layer keeps for the backward pass): each is rounded to fp16 after scaling by the power of two
+// that brings the largest magnitude into [1/2, 1), which leaves bit 14 of every fp16 zero; there
+// the eight bits of the exponent go, one each. Values within 2^-13 of the largest keep 11 bits
+// where bf16 keeps 8 (plain bf16 copies of these two tensors raised the error of the weight
+// gradients by a fifth), smaller ones an absolute error of 2^-25 of the largest. Where a magnitude
+// is 2^126 or more, infinite or NaN, the exponent is 255 and every value is the sign, the exponent
+// and six bits of mantissa of its fp32 form.
+__device__ __forceinline__ uint4 pack_block8(const float (&v)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(fabsf(v[i])));
+  const uint32_t e = __float_as_uint(m) >> 23;
+  uint32_t w[4];
+  if (e >= 253u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t u = __float_as_uint(v[2 * i + j]);
+        if ((u & 0x7fffffffu) > 0x7f800000u) u |= 0x00400000u;  // a NaN stays one when cut
+        h[j] = ((u >> 16) & 0x8000u) | 0x4000u | ((u >> 17) & 0x3fffu);
+      }
+      w[i] = h[0] | (h[1] << 16);
+    }
+  } else {
+    const float scale = __uint_as_float((253u - e) << 23);  // 2^(126 - e)
+    const uint32_t bits = (e & 15u) | ((e >> 4) << 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h;
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(v[2 * i + 1] * scale), "f"(v[2 * i] * scale));
+      w[i] = h | (((bits >> i) << 14) & 0x40004000u);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void unpack_block8(const uint4& q, float (&v)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bits |= ((w[i] & 0x40004000u) >> 14) << i;
+  const uint32_t e = (bits | (bits >> 12)) & 0xffu;
+  if (e == 255u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t h = w[i] >> (16 * j);
+        v[2 * i + j] = __uint_as_float(((h & 0x8000u) << 16) | ((h & 0x3fffu) << 17));
+      }
+  } else {
+    const float scale = __uint_as_float((e + 1u) << 23);  // 2^(e - 126)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = w[i] & 0xbfffbfffu;
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+      v[2 * i] = f.x * scale;
+      v[2 * i + 1] = f.y * scale;
+    }
+  }
+}
+
+// Tiled bulk tensor copies global -> shared of three and four dimensions, completion counted on
+// `bar` in bytes; the _pair forms land in this CTA and count on an mbarrier of either CTA of a
+// pair (a shared::cluster address).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int32_t x, int32_t y,
                                             int32_t z, uint32_t bar) {
   asm volatile(
@@ -31,6 +113,72 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int3
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int32_t x, int32_t y,
+                                            int32_t z, int32_t w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap, int32_t x,
+                                                 int32_t y, int32_t z, uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void* tmap, int32_t x,
+                                                 int32_t y, int32_t z, int32_t w,
+                                                 uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(cluster_bar)
+      : "memory");
+}
+
+// Clusters: the CTAs of this one, a store into another CTA's shared memory, and the bounded wait
+// (whole warp) on a barrier that other CTAs arrive on, which also makes their stores visible.
+__device__ __forceinline__ uint32_t cluster_nctas() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_smem, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_smem), "r"(v) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cluster_warp(uint32_t bar, uint32_t parity,
+                                                       volatile int* abort, int* status) {
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  for (int it = 0;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
+    int give_up = 0;
+    if ((threadIdx.x & 31) == 0 && it >= 256)
+      give_up = (*abort != 0) || (global_timer_ns() - t0 > kWaitLimitNs);
+    give_up = __shfl_sync(0xffffffffu, give_up, 0);
+    if (give_up) {
+      if ((threadIdx.x & 31) == 0 && *abort == 0) {
+        set_device_error(status, MOE_DEVERR_TIMEOUT);
+        *abort = 1;
+      }
+      return false;
+    }
+  }
 }
 
 }  // namespace moe

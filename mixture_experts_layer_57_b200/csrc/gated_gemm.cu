@@ -1,7 +1,7 @@
 // The products of the gated expert FFN over expert-major rows on sm_100a tensor cores (tcgen05 +
 // TMEM + TMA), forward and backward. For every row r of expert e's segment:
 //     up      h[r, i] = act(zg) zu,  zg = Wg[e][i] . x[r] + bg[e, i],  zu likewise with Wu, bu
-//             (training also writes a = act(zg) and q = zu act'(zg))
+//             (training also writes a = act(zg) and q = zu act'(zg), as blocks of eight values)
 //     down    y[r, m] = Wd[e][m] . h[r] + bd[e, m]
 //     hidden  dh[r, i] = sum_m dy[r, m] Wd[e][m, i];  dg = dh q,  du = dh a
 //     input   dx[r, j] = sum_i dg[r, i] Wg[e][i, j] + du[r, i] Wu[e][i, j]
@@ -16,12 +16,15 @@
 // eight shuffles per 16 tokens give every lane zg and zu of one feature for eight tokens, so the
 // activation and the product cost no extra pass, no extra accumulator and no shared memory.
 //
-// Schedule and roles as in the grouped GEMM: persistent CTAs walk tiles (expert, feature tile,
+// Hidden: the epilogue reads a and q, and loads them for its next 16 tokens while it works on these.
+//
+// Schedule and roles as in the grouped GEMM: persistent clusters walk tiles (expert, feature tile,
 // token tile); warp 0 issues TMA into a ring of stages (64 of K each, 128-byte swizzle), one
-// thread of warp 1 issues the MMAs into one of two accumulators, warps 2..9 are the epilogue of the
-// tile before. Every wait is bounded; on expiry MOE_DEVERR_TIMEOUT is recorded, the other roles
+// thread of warp 1 issues the MMAs into one of two accumulators, warps 2..13 are the epilogue of
+// the tile before. Every wait is bounded; on expiry MOE_DEVERR_TIMEOUT is recorded, the other roles
 // stop, in-flight copies and MMAs are drained and TMEM is freed.
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "gated.cuh"
@@ -33,11 +36,12 @@ namespace {
 constexpr int kBM = 128;         // A rows per tile and CTA
 constexpr int kBK = 64;          // K per stage: one 128-byte swizzle row of bf16
 constexpr int kUmmaK = 16;       // K per tcgen05.mma (kind::f16)
-constexpr int kThreads = 320;    // 10 warps: TMA, MMA, 8 epilogue
-constexpr int kEpiWarps = 8;
+constexpr int kEpiSets = 3;      // epilogue warps for each quarter of the accumulator's lanes
+constexpr int kEpiWarps = 4 * kEpiSets;
+constexpr int kThreads = 64 + 32 * kEpiWarps;  // TMA, MMA, epilogue
 constexpr int kEpiTileBytes = 16 * 32 * 4;  // per epilogue warp: 16 tokens x 32 features, fp32
 constexpr int kBoxL = 64, kBoxS = 16;       // token rows of the two TMA box heights
-constexpr int kRingBytes = 200 * 1024;
+constexpr int kRingBytes = 193 * 1024;
 
 enum Op { kUp = 0, kDown = 1, kHidden = 2, kInput = 3 };
 
@@ -53,6 +57,8 @@ struct GemmParams {
   int out_bf16;              // kDown, kInput
   int act;
   int* status;
+  int joint;    // kUp: one box of a four-dimensional map brings gate and up rows together
+  int up_first; // kUp: in that map the up projection's rows come first
 };
 
 // A and B of each product; the token operand with both box heights.
@@ -60,27 +66,43 @@ struct GemmMaps {
   CUtensorMap a0, a1, b0l, b0s, b1l, b1s;
 };
 
+// How CTAs share a tile.
+//   kPair    two CTAs on two SMs, MMAs of M = 256 (cta_group::2): each holds 128 A rows, half of
+//            the token rows and its half of the accumulator, so each token row is loaded once per
+//            pair
+//   kSplit   a cluster of S = 1, 2, 4 or 8 CTAs, each with its share of the K blocks; each CTA then
+//            finishes every S-th group of 16 tokens, for which the others write their partial sums
+//            into its shared memory
+enum Mode { kPair = 0, kSplit = 1 };
+constexpr int kMaxSplit = 8;
+constexpr int kPartChunk = 16 * kBM * 4;  // partial sums of 16 tokens
+
 // FT: A tiles of 128 rows per CTA tile, each with its own accumulator, that share the token rows
-// of a stage.
-template <int OP, int BN, int FT>
+// of a stage. Two sets of accumulators: a tile's MMAs run while the one before is finished.
+template <int OP, int BN, int FT, int MODE>
 struct GemmCfg {
   static constexpr bool kAMn = OP == kHidden || OP == kInput;  // weights read MN-major
   static constexpr int kPhases = OP == kInput ? 2 : 1;
   static constexpr int kFeat = (OP == kUp ? kBM / 2 : kBM);    // output features per A tile
-  static constexpr int kTileFeat = kFeat * FT;
+  static constexpr int kTileFeat = kFeat * FT * (MODE == kPair ? 2 : 1);
   static constexpr int kABytes = FT * kBM * kBK * 2;
-  static constexpr int kStageBytes = kABytes + BN * kBK * 2;
-  static constexpr int kStagesFit = kRingBytes / kStageBytes;
+  static constexpr int kBRows = MODE == kPair ? BN / 2 : BN;   // token rows per CTA and stage
+  static constexpr int kStageBytes = kABytes + kBRows * kBK * 2;
+  // kSplit: the other CTAs' sums for this one's groups of 16 tokens, of which a tile has at most
+  // eight: seven of one group for S = 8, three of two for 4, one of four for 2
+  static constexpr int kPartBytes = MODE == kSplit ? (kMaxSplit - 1) * kPartChunk : 0;
+  static constexpr int kStagesFit = (kRingBytes - kPartBytes) / kStageBytes;
   static constexpr int kStages = kStagesFit > 12 ? 12 : kStagesFit;
   static constexpr int kAccCols = FT * BN;
-  static constexpr int kTmemCols = 2 * kAccCols < 32 ? 32 : 2 * kAccCols;
-  static_assert(kTmemCols <= 512, "two accumulator buffers must fit TMEM");
+  static constexpr int kTmemCols = 2 * kAccCols;
+  static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM");
+  static_assert(MODE != kSplit || (FT == 1 && BN <= 128), "split tiles");
   static constexpr int kBarBytes = 8 * 64;
   static constexpr int kAuxBytes = kBarBytes + 16 + 2 * 4 * (MOE_MAX_EXPERTS + 1);
   static constexpr int kSmemBytes =
-      1024 + kStages * kStageBytes + kEpiWarps * kEpiTileBytes + kAuxBytes;
+      1024 + kStages * kStageBytes + kPartBytes + kEpiWarps * kEpiTileBytes + kAuxBytes;
   static_assert(kStageBytes % 1024 == 0, "stage tiles must stay 1024-byte aligned");
-  static_assert(2 * kStages + 5 <= 64, "barrier area too small");
+  static_assert(kStages >= 3 && 2 * kStages + 7 <= 64, "stages");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
@@ -117,8 +139,9 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, int* s
   }
 }
 
-// The mbarriers of one CTA: S stage-full, S stage-empty, 2 accumulator-full, 2 accumulator-empty
-// and one drain barrier, 8 bytes each from `base`.
+// The mbarriers of one CTA: S stage-full, S stage-empty, 2 accumulator-full, 2 accumulator-empty,
+// one drain barrier, and kSplit's two: the others' partial sums are written, and they have read
+// this CTA's. 8 bytes each from `base`.
 struct Bars {
   uint32_t base;
   int S;
@@ -127,8 +150,11 @@ struct Bars {
   __device__ __forceinline__ uint32_t tfull(int a) const { return base + 8u * (2 * S + a); }
   __device__ __forceinline__ uint32_t tempty(int a) const { return base + 8u * (2 * S + 2 + a); }
   __device__ __forceinline__ uint32_t drain() const { return base + 8u * (2 * S + 4); }
+  __device__ __forceinline__ uint32_t part_full() const { return base + 8u * (2 * S + 5); }
+  __device__ __forceinline__ uint32_t part_free() const { return base + 8u * (2 * S + 6); }
 };
 
+// Position in the stage ring.
 struct Ring {
   int stage = 0;
   uint32_t phase = 0;
@@ -183,8 +209,28 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return (uint32_t)f32_to_bf16_rn(lo) | ((uint32_t)f32_to_bf16_rn(hi) << 16);
 }
 
+// One box into this CTA's shared memory, counted on `bar` (a pair's loads count on the barrier of
+// its first CTA).
+template <int MODE>
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+  if constexpr (MODE == kPair) tma_load_2d_pair(dst, m, x, y, bar);
+  else tma_load_2d(dst, m, x, y, bar);
+}
+template <int MODE>
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z,
+                                        uint32_t bar) {
+  if constexpr (MODE == kPair) tma_load_3d_pair(dst, m, x, y, z, bar);
+  else tma_load_3d(dst, m, x, y, z, bar);
+}
+template <int MODE>
+__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* m, int x, int y, int z,
+                                        int w, uint32_t bar) {
+  if constexpr (MODE == kPair) tma_load_4d_pair(dst, m, x, y, z, w, bar);
+  else tma_load_4d(dst, m, x, y, z, w, bar);
+}
+
 // Loads the A tile(s) of one stage: feature f0 of expert e on, K block kb of product `ph`.
-template <int OP, int FT>
+template <int OP, int FT, int MODE>
 __device__ __forceinline__ void load_a(uint32_t sa, const GemmMaps& m, const GemmParams& p, int ph,
                                        int e, int f0, int kb, uint32_t bar) {
 #pragma unroll
@@ -194,149 +240,241 @@ __device__ __forceinline__ void load_a(uint32_t sa, const GemmMaps& m, const Gem
       // rows past this expert's features belong to the next expert or are out of range; the
       // epilogue masks them
       const int w_row = e * p.n_out + f0 + i * (kBM / 2);
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        tma_load_2d(sai + g * 4096, &m.a0, kb * kBK, w_row + g * 16, bar);
-        tma_load_2d(sai + g * 4096 + 2048, &m.a1, kb * kBK, w_row + g * 16, bar);
+      if (p.joint) {
+        load_4d<MODE>(sai, &m.a0, kb * kBK, 0, 0, w_row >> 4, bar);
+      } else {
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          load_2d<MODE>(sai + g * 4096, &m.a0, kb * kBK, w_row + g * 16, bar);
+          load_2d<MODE>(sai + g * 4096 + 2048, &m.a1, kb * kBK, w_row + g * 16, bar);
+        }
       }
     } else if constexpr (OP == kDown) {
-      tma_load_2d(sai, &m.a0, kb * kBK, e * p.n_out + f0 + i * kBM, bar);
+      load_2d<MODE>(sai, &m.a0, kb * kBK, e * p.n_out + f0 + i * kBM, bar);
     } else {
       const CUtensorMap* a = ph == 0 ? &m.a0 : &m.a1;
       // three dimensions, so that K rows past this expert's are zero and not the next expert's
       // (whose weights may be infinite or NaN)
-      tma_load_3d(sai, a, f0 + i * kBM, kb * kBK, e, bar);
-      tma_load_3d(sai + kBM * kBK, a, f0 + i * kBM + 64, kb * kBK, e, bar);
+      load_3d<MODE>(sai, a, f0 + i * kBM, kb * kBK, e, bar);
+      load_3d<MODE>(sai + kBM * kBK, a, f0 + i * kBM + 64, kb * kBK, e, bar);
     }
   }
 }
 
 // Loads n token rows (a multiple of 16) from row0 on, in boxes of 64 rows and then of 16.
+template <int MODE>
 __device__ __forceinline__ void load_b(uint32_t sb, const CUtensorMap* l, const CUtensorMap* s,
                                        int kb, int row0, int n, uint32_t bar) {
   int r = 0;
-  for (; r + kBoxL <= n; r += kBoxL) tma_load_2d(sb + r * 128, l, kb * kBK, row0 + r, bar);
-  for (; r < n; r += kBoxS) tma_load_2d(sb + r * 128, s, kb * kBK, row0 + r, bar);
+#pragma unroll 1
+  for (; r + kBoxL <= n; r += kBoxL) load_2d<MODE>(sb + r * 128, l, kb * kBK, row0 + r, bar);
+#pragma unroll 1
+  for (; r < n; r += kBoxS) load_2d<MODE>(sb + r * 128, s, kb * kBK, row0 + r, bar);
 }
 
-// Epilogue of one A tile (features f0 .. f0 + kFeat): this warp's lane quarter of the accumulator
-// at acc, alternate 16-token chunks by `half`, staged through `st` so that rows leave in 16-byte
-// stores.
-template <int OP>
-__device__ __forceinline__ void epilogue(const Tile& tl, int f0, const GemmParams& p, uint32_t acc,
-                                         int quarter, int half, int lane, uint8_t* st) {
-  const uint32_t taddr = acc + ((uint32_t)(quarter * 32) << 16);
-  if constexpr (OP == kUp) {
-    const int j = lane & 15, up = lane >> 4;
-    const int fw = f0 + quarter * 16;  // first feature of this warp
-    const int f = fw + j;
-    const bool f_ok = f < p.n_out;
-    const int64_t bi = (int64_t)tl.e * p.n_out + f;
-    const float bg = p.bias0 != nullptr && f_ok ? bf16_to_f32(p.bias0[bi]) : 0.0f;
-    const float bu = p.bias1 != nullptr && f_ok ? bf16_to_f32(p.bias1[bi]) : 0.0f;
-    uint16_t* s16 = reinterpret_cast<uint16_t*>(st);  // [3][16 tokens][16 features]
-    const bool save = p.out1 != nullptr;
-    for (int c0 = half * 16; c0 < tl.n_valid; c0 += 32) {
-      uint32_t r[16];
-      tmem_ld_32x32b_x16(taddr + (uint32_t)c0, r);
-      tmem_ld_wait();
-      const int nc = min(16, tl.n_valid - c0);
+// Token columns of a tile's MMAs: its rows rounded up to what N allows (M = 256: multiples of 32).
+template <int MODE>
+__device__ __forceinline__ int mma_n(int n_valid) {
+  return MODE == kPair ? (n_valid + 31) & ~31 : (n_valid + 15) & ~15;
+}
+
+// Which groups of 16 tokens of a tile this CTA finishes (kSplit: every `width`-th from `rank` on).
+struct Share {
+  int rank, width;
+  const float* part;
+  // groups of a full tile that one CTA finishes
+  __device__ __forceinline__ int groups(int bn) const { return (bn / 16 + width - 1) / width; }
+};
+
+// Waits for the tcgen05.ld into r; the operands keep every use of r behind it.
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+
+// What an epilogue warp of kHidden reads besides the accumulator: a and q of 16 tokens and 32
+// features, eight features of one token to each of two loads a lane.
+struct HiddenIn {
+  uint4 a[2], q[2];
+};
+__device__ __forceinline__ void load_hidden_in(HiddenIn& in, const GemmParams& p, const Tile& tl,
+                                               int fw, int c0, int lane) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        // gate lanes keep tokens 0..7 and give 8..15, up lanes the other way round
-        const float own = __uint_as_float(up ? r[8 + i] : r[i]);
-        const float got = __shfl_xor_sync(0xffffffffu, __uint_as_float(up ? r[i] : r[8 + i]), 16);
-        const float zg = (up ? got : own) + bg;
-        const float zu = (up ? own : got) + bu;
-        float a, da;
-        gate_act<true>(zg, p.act, a, da);
-        const int at = (up * 8 + i) * 16 + j;
-        s16[at] = f32_to_bf16_rn(a * zu);
-        if (save) {
-          s16[256 + at] = f32_to_bf16_rn(a);
-          s16[512 + at] = f32_to_bf16_rn(zu * da);
-        }
-      }
-      __syncwarp();
-      const int row = lane >> 1, ff = fw + 8 * (lane & 1);
-      if (row < nc && ff < p.n_out) {
-        const int64_t o = (int64_t)(tl.row0 + c0 + row) * p.n_out + ff;
-        const uint4* s4 = reinterpret_cast<const uint4*>(st) + lane;
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out0) + o) = s4[0];
-        if (save) {
-          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out1) + o) = s4[32];
-          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out2) + o) = s4[64];
-        }
-      }
-      __syncwarp();
-    }
-  } else {
-    const int fw = f0 + quarter * 32;
-    const int f = fw + lane;
-    const float bv = OP == kDown && p.bias0 != nullptr && f < p.n_out
-                         ? bf16_to_f32(p.bias0[(int64_t)tl.e * p.n_out + f])
-                         : 0.0f;
-    float* s32 = reinterpret_cast<float*>(st);  // [16 tokens][32 features]
-    for (int c0 = half * 16; c0 < tl.n_valid; c0 += 32) {
-      uint32_t r[16];
-      tmem_ld_32x32b_x16(taddr + (uint32_t)c0, r);
-      tmem_ld_wait();
-      const int nc = min(16, tl.n_valid - c0);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) s32[c * 32 + lane] = __uint_as_float(r[c]) + bv;
-      __syncwarp();
-      if (OP != kHidden && !p.out_bf16) {
-#pragma unroll
-        for (int id = lane; id < 128; id += 32) {
-          const int row = id >> 3, ff = fw + 4 * (id & 7);
-          if (row < nc && ff < p.n_out)
-            *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out0) +
-                                       (int64_t)(tl.row0 + c0 + row) * p.n_out + ff) =
-                *reinterpret_cast<const float4*>(st + id * 16);
-        }
-      } else {
-        // 8 features of one token per lane
-#pragma unroll
-        for (int id = lane; id < 64; id += 32) {
-          const int row = id >> 2, ff = fw + 8 * (id & 3);
-          if (row < nc && ff < p.n_out) {
-            const int64_t o = (int64_t)(tl.row0 + c0 + row) * p.n_out + ff;
-            const float4 v0 = *reinterpret_cast<const float4*>(st + id * 32);
-            const float4 v1 = *reinterpret_cast<const float4*>(st + id * 32 + 16);
-            if constexpr (OP == kHidden) {
-              auto times = [&](const uint16_t* in) {
-                const uint4 s = *reinterpret_cast<const uint4*>(in + o);
-                uint4 w;
-                w.x = pack2(v0.x * __uint_as_float(s.x << 16), v0.y * __uint_as_float(s.x & 0xffff0000u));
-                w.y = pack2(v0.z * __uint_as_float(s.y << 16), v0.w * __uint_as_float(s.y & 0xffff0000u));
-                w.z = pack2(v1.x * __uint_as_float(s.z << 16), v1.y * __uint_as_float(s.z & 0xffff0000u));
-                w.w = pack2(v1.z * __uint_as_float(s.w << 16), v1.w * __uint_as_float(s.w & 0xffff0000u));
-                return w;
-              };
-              const uint4 du = times(p.in0), dg = times(p.in1);
-              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out0) + o) = dg;
-              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out1) + o) = du;
-            } else {
-              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out0) + o) =
-                  make_uint4(pack2(v0.x, v0.y), pack2(v0.z, v0.w), pack2(v1.x, v1.y), pack2(v1.z, v1.w));
-            }
-          }
-        }
-      }
-      __syncwarp();
+  for (int u = 0; u < 2; ++u) {
+    const int id = lane + 32 * u, row = c0 + (id >> 2), ff = fw + 8 * (id & 3);
+    if (row < tl.n_valid && ff < p.n_out) {
+      const int64_t o = (int64_t)(tl.row0 + row) * p.n_out + ff;
+      in.a[u] = *reinterpret_cast<const uint4*>(p.in0 + o);
+      in.q[u] = *reinterpret_cast<const uint4*>(p.in1 + o);
     }
   }
 }
 
-template <int OP, int BN, int FT>
+// Up projection: 16 tokens of this warp's 16 features; zg and zu of a feature lie in lanes half a
+// warp apart.
+__device__ __forceinline__ void finish_up(const Tile& tl, const GemmParams& p, const uint32_t (&r)[16],
+                                          int fw, int c0, float bg, float bu, int lane, uint8_t* st) {
+  const int j = lane & 15, hi = lane >> 4, up = hi ^ p.up_first;
+  uint16_t* s16 = reinterpret_cast<uint16_t*>(st);       // h: [16 tokens][16 features]
+  float* s32 = reinterpret_cast<float*>(st + 512);       // a, then q: the same, 16 floats between
+                                                         // tokens 7 and 8 (bank conflicts)
+  const bool save = p.out1 != nullptr;
+  float a[8], q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // the lower lanes keep tokens 0..7 and give 8..15, the upper ones the other way round
+    const float own = __uint_as_float(hi ? r[8 + i] : r[i]);
+    const float got = __shfl_xor_sync(0xffffffffu, __uint_as_float(hi ? r[i] : r[8 + i]), 16);
+    const float zg = (up ? got : own) + bg;
+    const float zu = (up ? own : got) + bu;
+    float da;
+    gate_act<true>(zg, p.act, a[i], da);
+    q[i] = zu * da;
+    s16[(hi * 8 + i) * 16 + j] = f32_to_bf16_rn(a[i] * zu);
+  }
+  const int row = lane >> 1, ff = fw + 8 * (lane & 1);
+  const bool mine = c0 + row < tl.n_valid && ff < p.n_out;
+  const int64_t o = (int64_t)(tl.row0 + c0 + row) * p.n_out + ff;
+  if (save) {
+    float* put = s32 + (hi * 8) * 16 + hi * 16 + j;
+    const float4* get = reinterpret_cast<const float4*>(s32 + lane * 8 + hi * 16);
+    auto store = [&](void* out) {
+      const float4 x = get[0], y = get[1];
+      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      if (mine) *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(out) + o) = pack_block8(v);
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) put[i * 16] = a[i];
+    __syncwarp();
+    store(p.out1);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) put[i * 16] = q[i];
+    __syncwarp();
+    store(p.out2);
+  } else {
+    __syncwarp();
+  }
+  if (mine)
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out0) + o) =
+        reinterpret_cast<const uint4*>(st)[lane];
+  __syncwarp();
+}
+
+// The other products: 16 tokens of this warp's 32 features, staged as fp32 so that rows leave in
+// 16-byte stores.
+template <int OP>
+__device__ __forceinline__ void finish(const Tile& tl, const GemmParams& p, const uint32_t (&r)[16],
+                                       int fw, int c0, float bv, const HiddenIn& in, int lane,
+                                       uint8_t* st) {
+  float* s32 = reinterpret_cast<float*>(st);  // [16 tokens][32 features]
+#pragma unroll
+  for (int c = 0; c < 16; ++c) s32[c * 32 + lane] = __uint_as_float(r[c]) + bv;
+  __syncwarp();
+  const int nc = min(16, tl.n_valid - c0);
+  if (OP != kHidden && !p.out_bf16) {
+#pragma unroll
+    for (int id = lane; id < 128; id += 32) {
+      const int row = id >> 3, ff = fw + 4 * (id & 7);
+      if (row < nc && ff < p.n_out)
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out0) +
+                                   (int64_t)(tl.row0 + c0 + row) * p.n_out + ff) =
+            *reinterpret_cast<const float4*>(st + id * 16);
+    }
+  } else {
+    // 8 features of one token per lane
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int id = lane + 32 * u, row = id >> 2, ff = fw + 8 * (id & 3);
+      if (row < nc && ff < p.n_out) {
+        const int64_t o = (int64_t)(tl.row0 + c0 + row) * p.n_out + ff;
+        const float4 v0 = *reinterpret_cast<const float4*>(st + id * 32);
+        const float4 v1 = *reinterpret_cast<const float4*>(st + id * 32 + 16);
+        if constexpr (OP == kHidden) {
+          auto times = [&](const uint4& block) {
+            float s[8];
+            unpack_block8(block, s);
+            return make_uint4(pack2(v0.x * s[0], v0.y * s[1]), pack2(v0.z * s[2], v0.w * s[3]),
+                              pack2(v1.x * s[4], v1.y * s[5]), pack2(v1.z * s[6], v1.w * s[7]));
+          };
+          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out0) + o) = times(in.q[u]);
+          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out1) + o) = times(in.a[u]);
+        } else {
+          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out0) + o) =
+              make_uint4(pack2(v0.x, v0.y), pack2(v0.z, v0.w), pack2(v1.x, v1.y), pack2(v1.z, v1.w));
+        }
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// Epilogue of a tile: this warp's lane quarter of its FT accumulators from acc on, every kEpiSets-th
+// group of 16 tokens (kSplit: of this CTA's groups, with the other CTAs' partial sums added in rank
+// order) from `set` on. The next group's accumulator columns, and for kHidden its a and q, are under
+// way while a group is finished; kHidden's first ones come in `in`.
+template <int OP, int BN, int FT, int MODE>
+__device__ __forceinline__ void epilogue(const Tile& tl, int f0, const GemmParams& p, uint32_t acc,
+                                         int quarter, int set, int lane, uint8_t* st,
+                                         const Share& sh, HiddenIn& in) {
+  using C = GemmCfg<OP, BN, FT, MODE>;
+  const int first = (MODE == kSplit ? sh.rank + set * sh.width : set) * 16;
+  const int next = (MODE == kSplit ? kEpiSets * sh.width : kEpiSets) * 16;
+  if (first >= tl.n_valid) return;
+  const uint32_t taddr = acc + ((uint32_t)(quarter * 32) << 16);
+  uint32_t r[16];
+  tmem_ld_32x32b_x16(taddr + (uint32_t)first, r);
+#pragma unroll 1
+  for (int j = 0; j < FT; ++j) {
+    const int fw = f0 + j * C::kFeat + quarter * (OP == kUp ? 16 : 32);  // first of this warp
+    const int f = fw + (OP == kUp ? lane & 15 : lane);
+    const int64_t bi = (int64_t)tl.e * p.n_out + f;
+    const bool f_ok = f < p.n_out;
+    const float b0 = p.bias0 != nullptr && f_ok ? bf16_to_f32(p.bias0[bi]) : 0.0f;
+    const float b1 = p.bias1 != nullptr && f_ok ? bf16_to_f32(p.bias1[bi]) : 0.0f;
+    const float* part = MODE == kSplit ? sh.part + set * (kPartChunk / 4) + quarter * 32 + lane : nullptr;
+#pragma unroll 1
+    for (int c0 = first; c0 < tl.n_valid; c0 += next) {
+      tmem_ld_wait16(r);
+      uint32_t v[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) v[c] = r[c];
+      const bool more = c0 + next < tl.n_valid;
+      const int nj = more ? j : j + 1, nc0 = more ? c0 + next : first;
+      if (nj < FT) tmem_ld_32x32b_x16(taddr + (uint32_t)(nj * BN + nc0), r);
+      if constexpr (MODE == kSplit) {
+        const int stride = sh.groups(BN) * (kPartChunk / 4);
+#pragma unroll 1
+        for (int s = 0; s + 1 < sh.width; ++s)
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            v[c] = __float_as_uint(__uint_as_float(v[c]) + part[s * stride + c * kBM]);
+        part += kEpiSets * (kPartChunk / 4);
+      }
+      if constexpr (OP == kUp) {
+        finish_up(tl, p, v, fw, c0, b0, b1, lane, st);
+      } else {
+        const HiddenIn cur = in;
+        if (OP == kHidden && nj < FT)
+          load_hidden_in(in, p, tl, f0 + nj * C::kFeat + quarter * 32, nc0, lane);
+        finish<OP>(tl, p, v, fw, c0, OP == kDown ? b0 : 0.0f, cur, lane, st);
+      }
+    }
+  }
+}
+
+template <int OP, int BN, int FT, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmParams p) {
-  using C = GemmCfg<OP, BN, FT>;
+  using C = GemmCfg<OP, BN, FT, MODE>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t base_addr = (raw_addr + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (base_addr - raw_addr);
-  uint8_t* epi_tiles = base + C::kStages * C::kStageBytes;
+  float* part = reinterpret_cast<float*>(base + C::kStages * C::kStageBytes);
+  uint8_t* epi_tiles = base + C::kStages * C::kStageBytes + C::kPartBytes;
   uint8_t* aux = epi_tiles + kEpiWarps * kEpiTileBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(aux);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(aux + C::kBarBytes);
@@ -348,6 +486,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   constexpr int S = C::kStages;
   const Bars B{smem_u32(bars), S};
+  // CTAs that share a tile, this CTA's rank among them, and the tile walk's start and step
+  const int width = (int)cluster_nctas();
+  const int rank = (int)cluster_ctarank();
+  const int first = (int)blockIdx.x / width, step = (int)gridDim.x / width;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -356,26 +498,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(B.tfull(a), 1);
-      mbar_init(B.tempty(a), kEpiWarps * 32);
+      mbar_init(B.tempty(a), (MODE == kPair ? 2 : 1) * kEpiWarps * 32);
     }
     mbar_init(B.drain(), 1);
+    mbar_init(B.part_full(), (width > 1 ? width - 1 : 1) * kEpiWarps * 32);
+    mbar_init(B.part_free(), (width > 1 ? width - 1 : 1) * kEpiWarps);
     *abort_flag = 0;
     fence_barrier_init();
   }
   pdl_wait();
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_holder), C::kTmemCols);
-    tmem_relinquish();
+    if constexpr (MODE == kPair) {
+      tmem_alloc_pair(smem_u32(tmem_holder), C::kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_holder), C::kTmemCols);
+      tmem_relinquish();
+    }
   }
   const int n_ftiles = (p.n_out + C::kTileFeat - 1) / C::kTileFeat;
   if (warp == 2) build_tile_list<BN>(p, n_ftiles, prefix, seg, lane);
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  cluster_sync();  // barriers initialised (and a pair's TMEM allocated) in every CTA
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const int total_tiles = prefix[p.E];
   const int n_kb = (p.K + kBK - 1) / kBK;
   const int n_blocks = C::kPhases * n_kb;
+  // this CTA's K blocks (of both products of kInput, one after the other)
+  const int i0 = MODE == kSplit ? n_blocks * rank / width : 0;
+  const int i1 = MODE == kSplit ? n_blocks * (rank + 1) / width : n_blocks;
   auto tile_at = [&](int t) { return decode_tile<BN>(t, prefix, seg, p.E, C::kTileFeat); };
 
   if (warp == 0) {
@@ -384,10 +537,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring ring;
       int issued = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < total_tiles && ok; t += gridDim.x) {
+      for (int t = first; t < total_tiles && ok; t += step) {
         const Tile tl = tile_at(t);
-        const int n_b = (tl.n_valid + 15) & ~15;
-        for (int i = 0; i < n_blocks; ++i) {
+        const int n_b = mma_n<MODE>(tl.n_valid) / (MODE == kPair ? 2 : 1);
+        const int f0 = tl.f0 + (MODE == kPair ? rank * FT * C::kFeat : 0);
+        const int row0 = tl.row0 + (MODE == kPair ? rank * n_b : 0);
+        const uint32_t tx = C::kABytes + n_b * 128;
+        for (int i = i0; i < i1; ++i) {
           if (!mbar_wait_bounded(B.empty(ring.stage), ring.phase ^ 1u, abort_flag, p.status)) {
             ok = false;
             break;
@@ -395,33 +551,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int ph = C::kPhases == 2 && i >= n_kb ? 1 : 0;
           const int kb = i - ph * n_kb;
           const uint32_t sa = base_addr + ring.stage * C::kStageBytes;
-          mbar_arrive_expect_tx(B.full(ring.stage), C::kABytes + n_b * 128);
-          load_a<OP, FT>(sa, maps, p, ph, tl.e, tl.f0, kb, B.full(ring.stage));
-          load_b(sa + C::kABytes, ph ? &maps.b1l : &maps.b0l, ph ? &maps.b1s : &maps.b0s, kb,
-                 tl.row0, n_b, B.full(ring.stage));
+          uint32_t bar = B.full(ring.stage);
+          if constexpr (MODE == kPair) {
+            if (rank == 0) mbar_arrive_expect_tx(bar, 2 * tx);  // both CTAs' bytes
+            bar = cluster_addr(bar, 0);
+          } else {
+            mbar_arrive_expect_tx(bar, tx);
+          }
+          load_a<OP, FT, MODE>(sa, maps, p, ph, tl.e, f0, kb, bar);
+          load_b<MODE>(sa + C::kABytes, ph ? &maps.b1l : &maps.b0l, ph ? &maps.b1s : &maps.b0s, kb,
+                       row0, n_b, bar);
           ++issued;
           ring.next(S);
         }
       }
-      // drain: the last min(issued, S) loads may still be landing
-      for (int i = max(0, issued - S); i < issued; ++i)
-        wait_drain(B.full(i % S), (uint32_t)((i / S) & 1), p.status);
+      // drain: the last min(issued, S) loads may still be landing (a pair's first CTA counts both
+      // CTAs' copies; the other stays resident until the cluster barrier below)
+      if (MODE != kPair || rank == 0)
+        for (int i = max(0, issued - S); i < issued; ++i)
+          wait_drain(B.full(i % S), (uint32_t)((i / S) & 1), p.status);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    if (lane == 0 && (MODE != kPair || rank == 0)) {
       Ring ring;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < total_tiles && ok; t += gridDim.x) {
+      for (int t = first; t < total_tiles && ok; t += step) {
         if (!mbar_wait_bounded(B.tempty(acc), acc_phase ^ 1u, abort_flag, p.status)) break;
         tc_fence_after();
         const Tile tl = tile_at(t);
-        const uint32_t idesc =
-            idesc_bf16_f32_major(kBM, (tl.n_valid + 15) & ~15, C::kAMn, false);
+        const uint32_t idesc = idesc_bf16_f32_major(MODE == kPair ? 2 * kBM : kBM,
+                                                    mma_n<MODE>(tl.n_valid), C::kAMn, false);
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * C::kAccCols);
-        for (int i = 0; i < n_blocks; ++i) {
+        for (int i = i0; i < i1; ++i) {
           if (!mbar_wait_bounded(B.full(ring.stage), ring.phase, abort_flag, p.status)) {
             ok = false;
             break;
@@ -435,51 +599,101 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t saj = sa + j * (kBM * kBK * 2);
             const uint64_t adesc = C::kAMn ? smem_desc_sw128_mn(saj) : smem_desc_sw128(saj);
 #pragma unroll
-            for (int kk = 0; kk < kBK / kUmmaK; ++kk)
-              tc_mma_bf16(d_tmem + (uint32_t)(j * BN), adesc + a_step * (uint64_t)kk,
-                          bdesc + (uint64_t)(2 * kk), idesc, (i | kk) != 0 ? 1u : 0u);
+            for (int kk = 0; kk < kBK / kUmmaK; ++kk) {
+              const uint32_t more = i != i0 || kk != 0 ? 1u : 0u;
+              if constexpr (MODE == kPair)
+                tc_mma_bf16_pair(d_tmem + (uint32_t)(j * BN), adesc + a_step * (uint64_t)kk,
+                                 bdesc + (uint64_t)(2 * kk), idesc, more);
+              else
+                tc_mma_bf16(d_tmem + (uint32_t)(j * BN), adesc + a_step * (uint64_t)kk,
+                            bdesc + (uint64_t)(2 * kk), idesc, more);
+            }
           }
-          tc_commit(B.empty(ring.stage));
+          if constexpr (MODE == kPair)
+            tc_commit_pair_both(B.empty(ring.stage), cluster_addr(B.empty(ring.stage), 1));
+          else
+            tc_commit(B.empty(ring.stage));
           ring.next(S);
         }
         if (!ok) break;
-        tc_commit(B.tfull(acc));
+        if constexpr (MODE == kPair)
+          tc_commit_pair_both(B.tfull(acc), cluster_addr(B.tfull(acc), 1));
+        else
+          tc_commit(B.tfull(acc));
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
       // drain every MMA this thread issued before TMEM is released
-      tc_commit(B.drain());
+      if constexpr (MODE == kPair) tc_commit_pair_local(B.drain());
+      else tc_commit(B.drain());
       wait_drain(B.drain(), 0, p.status);
     }
   } else {
-    // ---------------------------------------------------------- epilogue (warps 2..9)
+    // ---------------------------------------------------------- epilogue (warps 2..13)
     const int ew = warp - 2;
     const int quarter = warp & 3;  // TMEM lanes this warp may access
-    const int half = ew >> 2;
+    const int set = ew >> 2;
     uint8_t* st = epi_tiles + ew * kEpiTileBytes;
     int acc = 0;
-    uint32_t acc_phase = 0;
-    for (int t = blockIdx.x; t < total_tiles; t += gridDim.x) {
+    uint32_t acc_phase = 0, part_phase = 0;
+    for (int t = first; t < total_tiles; t += step) {
+      const Tile tl = tile_at(t);
+      const int f0 = tl.f0 + (MODE == kPair ? rank * FT * C::kFeat : 0);
+      HiddenIn in = {};
+      if constexpr (OP == kHidden)
+        load_hidden_in(in, p, tl, f0 + quarter * 32,
+                       (MODE == kSplit ? rank + set * width : set) * 16, lane);
       if (!mbar_wait_bounded_warp(B.tfull(acc), acc_phase, abort_flag, p.status)) break;
       tc_fence_after();
-      const Tile tl = tile_at(t);
-#pragma unroll 1
-      for (int j = 0; j < FT; ++j)
-        epilogue<OP>(tl, tl.f0 + j * C::kFeat, p,
-                     tmem_base + (uint32_t)(acc * C::kAccCols + j * BN), quarter, half, lane, st);
+      const uint32_t d_tmem = tmem_base + (uint32_t)(acc * C::kAccCols);
+      const Share sh{rank, width, part};
+      if (MODE == kSplit && width > 1) {
+        // hand the others their groups, once they have read the tile before's
+        if (!mbar_wait_cluster_warp(B.part_free(), part_phase ^ 1u, abort_flag, p.status)) break;
+        const uint32_t taddr = d_tmem + ((uint32_t)(quarter * 32) << 16);
+        const int groups = sh.groups(BN);
+        for (int g = set; g * 16 < tl.n_valid; g += kEpiSets) {
+          const int owner = g & (width - 1);  // the width is a power of two
+          if (owner == rank) continue;
+          const int slot = (rank < owner ? rank : rank - 1) * groups + g / width;
+          const uint32_t to = cluster_addr(smem_u32(part), owner) +
+                              (uint32_t)(slot * kPartChunk + (quarter * 32 + lane) * 4);
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(taddr + (uint32_t)(g * 16), r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 16; ++c) st_cluster_u32(to + (uint32_t)(c * kBM * 4), r[c]);
+        }
+        for (int s = 1; s < width; ++s)
+          mbar_arrive_cluster(cluster_addr(B.part_full(), (rank + s) & (width - 1)));
+        if (!mbar_wait_cluster_warp(B.part_full(), part_phase, abort_flag, p.status)) break;
+      }
+      epilogue<OP, BN, FT, MODE>(tl, f0, p, d_tmem, quarter, set, lane, st, sh, in);
+      if (MODE == kSplit && width > 1) {
+        __syncwarp();
+        if (lane == 0)
+          for (int s = 1; s < width; ++s)
+            mbar_arrive_cluster(cluster_addr(B.part_free(), (rank + s) & (width - 1)));
+      }
+      part_phase ^= 1u;
       tc_fence_before();
-      mbar_arrive(B.tempty(acc));
+      if constexpr (MODE == kPair)
+        mbar_arrive_cluster(cluster_addr(B.tempty(acc), 0));  // the first CTA issues the MMAs
+      else
+        mbar_arrive(B.tempty(acc));
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
   }
 
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  cluster_sync();  // no copy, commit, store or arrive targets another CTA after this
   pdl_trigger();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, C::kTmemCols);
+    if constexpr (MODE == kPair) tmem_dealloc_pair(tmem_base, C::kTmemCols);
+    else tmem_dealloc(tmem_base, C::kTmemCols);
   }
 }
 
@@ -490,8 +704,9 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// Weights [E, K, n] read MN-major in boxes of 64 features x 64 K rows of one expert.
-bool weight_map_mn(CUtensorMap* m, const void* ptr, int E, int K, int n) {
+// A bf16 map of the given extents (innermost first), byte strides of the outer dimensions and box.
+bool encode_map(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* extent,
+                const cuuint64_t* stride, const cuuint32_t* box) {
   static const EncodeTiledFn fn = []() -> EncodeTiledFn {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -501,34 +716,169 @@ bool weight_map_mn(CUtensorMap* m, const void* ptr, int E, int K, int n) {
       return nullptr;
     return reinterpret_cast<EncodeTiledFn>(f);
   }();
-  if (!fn) return false;
-  cuuint64_t gdim[3] = {(cuuint64_t)n, (cuuint64_t)K, (cuuint64_t)E};
-  cuuint64_t gstride[2] = {(cuuint64_t)n * 2, (cuuint64_t)n * K * 2};
-  cuuint32_t box[3] = {64, kBK, 1};
-  cuuint32_t estride[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), gdim, gstride, box,
-            estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn != nullptr &&
+         fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), extent,
+            stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int OP, int BN, int FT>
-cudaError_t launch_single(const GemmMaps& m, const GemmParams& p, cudaStream_t stream) {
-  auto kern = gated_gemm_kernel<OP, BN, FT>;
-  constexpr int smem = GemmCfg<OP, BN, FT>::kSmemBytes;
+// Weights [E, K, n] read MN-major in boxes of 64 features x 64 K rows of one expert.
+bool weight_map_mn(CUtensorMap* m, const void* ptr, int E, int K, int n) {
+  const cuuint64_t extent[3] = {(cuuint64_t)n, (cuuint64_t)K, (cuuint64_t)E};
+  const cuuint64_t stride[2] = {(cuuint64_t)n * 2, (cuuint64_t)n * K * 2};
+  const cuuint32_t box[3] = {64, kBK, 1};
+  return encode_map(m, ptr, 3, extent, stride, box);
+}
+
+// Both projections' rows [E * f, d] as one tensor [groups of 16 rows][2 projections][16 rows][d],
+// whose box of four groups is a whole A tile: the projections lie a fixed distance apart, which is
+// the stride of the second dimension from outside. Experts must start on a group (f % 16 == 0) and
+// the distance fit a stride (below 2^40); otherwise false, and 16-row boxes do.
+bool joint_map(CUtensorMap* m, const GatedFfn& g, int* up_first) {
+  const uintptr_t wg = (uintptr_t)g.w_gate, wu = (uintptr_t)g.w_up;
+  const uintptr_t lo = wg < wu ? wg : wu, apart = (wg < wu ? wu : wg) - lo;
+  if (g.f % 16 != 0 || apart == 0 || apart % 16 != 0 || apart >= ((uintptr_t)1 << 40)) return false;
+  *up_first = wu < wg ? 1 : 0;
+  const cuuint64_t row = (cuuint64_t)g.d * 2;
+  const cuuint64_t extent[4] = {(cuuint64_t)g.d, 16, 2, (cuuint64_t)g.E * g.f / 16};
+  const cuuint64_t stride[3] = {row, (cuuint64_t)apart, 16 * row};
+  const cuuint32_t box[4] = {kBK, 16, 2, 4};
+  return encode_map(m, (const void*)lo, 4, extent, stride, box);
+}
+
+// One way of running a product: the kernel, its clusters (CTAs of each, and how many of them the
+// device holds at once) and its shared memory.
+struct Config {
+  void (*kern)(GemmMaps, GemmParams);
+  int smem, width, slots;
+};
+
+cudaError_t launch_clusters(const Config& c, int64_t tiles, cudaStream_t stream, const GemmMaps& m,
+                            const GemmParams& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(tiles, c.slots) * c.width));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = c.smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)c.width;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, c.kern, m, p);
+  count_launch();
+  return e;
+}
+
+// The kernel for a mode in clusters of `width`, with its slots on this device (asked once per
+// kernel, width and device).
+template <int OP, int BN, int FT, int MODE>
+cudaError_t config_of(int width, Config* c) {
+  *c = Config{gated_gemm_kernel<OP, BN, FT, MODE>, GemmCfg<OP, BN, FT, MODE>::kSmemBytes, width, 0};
   static int attr_done[64] = {0};  // per instantiation and device
-  const cudaError_t e = ensure_dynamic_smem(kern, smem, attr_done);
+  cudaError_t e = ensure_dynamic_smem(c->kern, c->smem, attr_done);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(num_sms()), dim3(kThreads), smem, stream, m, p);
+  static std::atomic<int> slots[64][4];
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::atomic<int>& cached = slots[dev][width == 8 ? 3 : width / 2];
+  if ((c->slots = cached.load(std::memory_order_relaxed)) == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)width);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = c->smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)width;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaOccupancyMaxActiveClusters(&c->slots, c->kern, &cfg)) != cudaSuccess) return e;
+    if (c->slots < 1) return cudaErrorLaunchOutOfResources;
+    cached.store(c->slots, std::memory_order_relaxed);
+  }
+  return cudaSuccess;
+}
+
+template <int OP, int BN>
+cudaError_t config_of(int ft, int mode, int width, Config* c) {
+  if constexpr (BN <= 128)
+    if (mode == kSplit) return config_of<OP, BN, 1, kSplit>(width, c);
+  if constexpr (BN <= 128)
+    if (ft == 2) return config_of<OP, BN, 2, kPair>(2, c);
+  return config_of<OP, BN, 1, kPair>(2, c);
 }
 
 template <int OP>
+cudaError_t config_of(int bn, int ft, int mode, int width, Config* c) {
+  switch (bn) {
+    case 32: return config_of<OP, 32>(ft, mode, width, c);
+    case 64: return config_of<OP, 64>(ft, mode, width, c);
+    case 128: return config_of<OP, 128>(ft, mode, width, c);
+    default: return config_of<OP, 256>(ft, mode, width, c);
+  }
+}
+
+// Chooses how to run a product by an estimate of its time and launches it. Per K block a CTA takes
+// the larger of its loads' time (75 bytes/ns) and its MMAs' (2 cycles a token column and A tile);
+// rounds of tiles over the device's clusters multiply that; no way is faster than the weights come
+// from HBM, and of equal ones the first wins. So come
+//   - for many tiles of up to 128 rows, pairs with two A tiles, whose token rows cost the fewest
+//     loads (128 experts of 86 rows, d 1024, f 4096, up: 386 us; one A tile 431, single CTAs 444);
+//   - for more rows pairs with one A tile and 256 token columns (TMEM holds two sets of
+//     accumulators only of one such tile; 128 rows an expert on average, 160 at most, up: 429 us;
+//     two A tiles and one set, the epilogue not overlapped, 480);
+//   - splits where tiles are fewer than SMs (8 rows, d 8192 -> 2048: 19 us in clusters of 4, 27 of 2,
+//     44 unsplit).
+template <int OP>
 cudaError_t launch_op(const GemmMaps& m, const GemmParams& p, int64_t capacity_hint,
                       cudaStream_t stream) {
-  if (capacity_hint <= 16) return launch_single<OP, 16, 2>(m, p, stream);
-  if (capacity_hint <= 32) return launch_single<OP, 32, 2>(m, p, stream);
-  if (capacity_hint <= 64) return launch_single<OP, 64, 2>(m, p, stream);
-  if (capacity_hint <= 128) return launch_single<OP, 128, 2>(m, p, stream);
-  return launch_single<OP, 256, 1>(m, p, stream);
+  // rows of an expert and experts with rows, as far as the host knows
+  const int64_t rows = std::max<int64_t>(1, std::min(capacity_hint, p.rows_max));
+  const int64_t experts = std::min<int64_t>(p.E, p.rows_max);
+  const int feat = OP == kUp ? kBM / 2 : kBM;
+  const int64_t n_blocks = (int64_t)(OP == kInput ? 2 : 1) * ((p.K + kBK - 1) / kBK);
+  const double hbm_ns = (double)experts * p.n_out * n_blocks * kBK * (OP == kUp ? 4 : 2) / 6500.0;
+  Config best{};
+  int64_t best_tiles = 0;
+  double best_ns = 0;
+  auto consider = [&](int bn, int ft, int mode, int width) -> cudaError_t {
+    Config c{};
+    const cudaError_t e = config_of<OP>(bn, ft, mode, width, &c);
+    if (e != cudaSuccess) return e;
+    const int feats = feat * ft * (mode == kPair ? 2 : 1);
+    const int64_t tiles = experts * ((rows + bn - 1) / bn) * ((p.n_out + feats - 1) / feats);
+    const int64_t rounds = (tiles + c.slots - 1) / c.slots;
+    const double n = (double)std::min<int64_t>((rows + 15) / 16 * 16, bn);
+    const double load = (ft * kBM + (mode == kPair ? n / 2 : n)) * (kBK * 2) / 75.0;
+    const double mma = ft * 2 * n / 1.7;
+    const int ways = mode == kSplit ? width : 1;
+    double ns = (double)(rounds * ((n_blocks + ways - 1) / ways)) * std::max(load, mma);
+    if (mode == kSplit && width > 1) ns += 1500;  // the meeting of the partial sums
+    ns = std::max(ns, hbm_ns);
+    if (best.kern == nullptr || ns < best_ns) {
+      best = c;
+      best_tiles = tiles;
+      best_ns = ns;
+    }
+    return cudaSuccess;
+  };
+  cudaError_t e = cudaSuccess;
+  const int fit = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+  if (fit <= 128) e = consider(fit, 2, kPair, 2);
+  if (e == cudaSuccess) e = consider(fit, 1, kPair, 2);
+  if (fit == 256 && e == cudaSuccess) e = consider(128, 1, kPair, 2);
+  for (int width = 1; width <= kMaxSplit && n_blocks >= 4 * width; width *= 2)
+    if (e == cudaSuccess) e = consider(std::min(fit, 128), 1, kSplit, width);
+  if (e != cudaSuccess) return e;
+  return launch_clusters(best, best_tiles, stream, m, p);
 }
 
 // Both box heights of a token operand [rows, K].
@@ -543,13 +893,15 @@ cudaError_t enqueue_gated_up_bf16(const GatedFfn& g, void* h, void* saved_a, voi
                                   int* status, cudaStream_t stream) {
   if (g.rows_max == 0) return cudaSuccess;
   GemmMaps m;
-  if (!make_bf16_map_2d(&m.a0, g.w_gate, (int64_t)g.E * g.f, g.d, kBK, 16) ||
-      !make_bf16_map_2d(&m.a1, g.w_up, (int64_t)g.E * g.f, g.d, kBK, 16) ||
-      !token_maps(&m.b0l, &m.b0s, g.x, g.rows_max, g.d))
+  GemmParams p{};
+  p.joint = joint_map(&m.a0, g, &p.up_first) ? 1 : 0;
+  if (p.joint) m.a1 = m.a0;
+  else if (!make_bf16_map_2d(&m.a0, g.w_gate, (int64_t)g.E * g.f, g.d, kBK, 16) ||
+           !make_bf16_map_2d(&m.a1, g.w_up, (int64_t)g.E * g.f, g.d, kBK, 16))
     return cudaErrorInvalidValue;
+  if (!token_maps(&m.b0l, &m.b0s, g.x, g.rows_max, g.d)) return cudaErrorInvalidValue;
   m.b1l = m.b0l;
   m.b1s = m.b0s;
-  GemmParams p{};
   p.offsets = g.offsets; p.E = g.E; p.n_out = g.f; p.K = g.d; p.rows_max = g.rows_max;
   p.bias0 = (const uint16_t*)g.b_gate; p.bias1 = (const uint16_t*)g.b_up;
   p.out0 = h; p.out1 = saved_a; p.out2 = saved_q; p.act = g.act; p.status = status;

@@ -312,3 +312,47 @@ def test_gated_layer_from_router_to_combine(cuda_ok):
     assert total > 1.0 and abs(norm.item() - total) <= 2.0 ** -19 * total
     for n, t in zip(names, before):
         assert bool(((g[n].double() - t / (total + 1e-6)).abs() <= 2.0 ** -19 * t.abs() / total).all()), n
+
+
+@pytest.mark.parametrize("most", [1, 30, 64, 100, 200])
+def test_bf16_many_feature_tiles(cuda_ok, most):
+    # enough tiles to fill the device several times: pairs with two weight tiles up to 128 rows
+    gen = torch.Generator().manual_seed(most)
+    counts = torch.randint(most + 1, (40,), generator=gen).tolist()
+    counts[3], counts[7] = 0, most
+    c = make(40, counts, 520, 1032, torch.bfloat16, seed=most, first=1)
+    got, kept = run(c, "gelu")
+    compare(c, got, "gelu", kept)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 33, 64, 100, 128])
+def test_bf16_dense_block_split_sums(cuda_ok, rows):
+    # few tiles and long sums: every product is split over clusters
+    c = make(1, [rows], 1024, 2056, torch.bfloat16, seed=rows)
+    got, kept = run(c, "silu")
+    compare(c, got, "silu", kept)
+
+
+def test_bf16_small_and_large_scales(cuda_ok):
+    # what the forward pass keeps has a range of its own: activations far from 1 on either side
+    for std in (2.0 ** -60, 2.0 ** -20, 2.0 ** 20, 2.0 ** 40):
+        c = make(2, [33, 60], 64, 72, torch.bfloat16, bias=False, seed=17)
+        c["w_up"].mul_(std)
+        got, kept = run(c, "silu")
+        compare(c, got, "silu", kept)
+
+
+def test_bf16_infinity_in_one_feature(cuda_ok):
+    # an infinite up weight makes its feature's column infinite or NaN and no other
+    c = make(1, [40], 64, 128, torch.bfloat16, bias=False, seed=18)
+    clean, kept = run(c, "silu")
+    c["w_up"][0, 5] = float("inf")
+    got, bad = run(c, "silu")
+    keep = torch.arange(128, device="cuda") != 5
+    assert torch.equal(bad["h"][:40, keep], kept["h"][:40, keep])
+    assert not bool(torch.isfinite(bad["h"][:40, 5]).any())
+    # its neighbours share an exponent with it and keep 7 bits there: 2^-7 of each in their gradients
+    near = keep & (torch.arange(128, device="cuda") < 8)
+    far = torch.arange(128, device="cuda") >= 8
+    assert torch.equal(got["dw_up"][0, far], clean["dw_up"][0, far])
+    assert bool(torch.isfinite(got["dw_up"][0, near]).all())
