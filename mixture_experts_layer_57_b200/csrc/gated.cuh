@@ -140,6 +140,50 @@ __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void* tmap,
       : "memory");
 }
 
+// Two values rounded to bf16 in one instruction (conversions are slow one by one: 64 a lane bounded
+// the weight-gradient kernel's epilogue).
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Waits for the tcgen05.ld into r; the operands keep every use of r behind it.
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+
+// mbar_wait_bounded_warp, with a first try before the timer is read.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
+                                               int* status) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+         mbar_wait_bounded_warp(bar, parity, abort, status);
+}
+
+// Store of a box from shared memory (what lies outside the tensor is not written), in this thread's
+// current bulk group.
+__device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int32_t x, int32_t y,
+                                             int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// At most N of this thread's bulk groups have not read their shared memory yet / are not done.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// Makes this thread's shared-memory writes visible to TMA and MMA reads that follow.
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // Clusters: the CTAs of this one, a store into another CTA's shared memory, and the bounded wait
 // (whole warp) on a barrier that other CTAs arrive on, which also makes their stores visible.
 __device__ __forceinline__ uint32_t cluster_nctas() {
@@ -161,8 +205,26 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
       : "memory");
   return ok != 0;
 }
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort,
+                                                  int* status) {  // one thread
+#pragma unroll 1
+  for (int i = 0; i < 256; ++i)
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait_cluster(bar, parity)) {
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      set_device_error(status, MOE_DEVERR_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
 __device__ __forceinline__ bool mbar_wait_cluster_warp(uint32_t bar, uint32_t parity,
                                                        volatile int* abort, int* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
   const uint64_t t0 = global_timer_ns();
 #pragma unroll 1
   for (int it = 0;; ++it) {
@@ -180,5 +242,10 @@ __device__ __forceinline__ bool mbar_wait_cluster_warp(uint32_t bar, uint32_t pa
     }
   }
 }
+
+// A tensor map of the given extents (innermost first, in elements), byte strides of the outer
+// dimensions and box, 128-byte swizzle (host).
+bool gated_tensor_map(CUtensorMap* m, const void* ptr, bool bf16, int rank, const cuuint64_t* extent,
+                      const cuuint64_t* stride, const cuuint32_t* box);
 
 }  // namespace moe

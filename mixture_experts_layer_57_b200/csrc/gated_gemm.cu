@@ -205,10 +205,6 @@ __device__ __forceinline__ void build_tile_list(const GemmParams& p, int n_ftile
   }
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  return (uint32_t)f32_to_bf16_rn(lo) | ((uint32_t)f32_to_bf16_rn(hi) << 16);
-}
-
 // One box into this CTA's shared memory, counted on `bar` (a pair's loads count on the barrier of
 // its first CTA).
 template <int MODE>
@@ -286,14 +282,6 @@ struct Share {
   __device__ __forceinline__ int groups(int bn) const { return (bn / 16 + width - 1) / width; }
 };
 
-// Waits for the tcgen05.ld into r; the operands keep every use of r behind it.
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
-}
-
 // What an epilogue warp of kHidden reads besides the accumulator: a and q of 16 tokens and 32
 // features, eight features of one token to each of two loads a lane.
 struct HiddenIn {
@@ -321,7 +309,7 @@ __device__ __forceinline__ void finish_up(const Tile& tl, const GemmParams& p, c
   float* s32 = reinterpret_cast<float*>(st + 512);       // a, then q: the same, 16 floats between
                                                          // tokens 7 and 8 (bank conflicts)
   const bool save = p.out1 != nullptr;
-  float a[8], q[8];
+  float a[8], q[8], h[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     // the lower lanes keep tokens 0..7 and give 8..15, the upper ones the other way round
@@ -332,7 +320,13 @@ __device__ __forceinline__ void finish_up(const Tile& tl, const GemmParams& p, c
     float da;
     gate_act<true>(zg, p.act, a[i], da);
     q[i] = zu * da;
-    s16[(hi * 8 + i) * 16 + j] = f32_to_bf16_rn(a[i] * zu);
+    h[i] = a[i] * zu;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const uint32_t two = pack_bf16x2(h[i], h[i + 1]);
+    s16[(hi * 8 + i) * 16 + j] = (uint16_t)two;
+    s16[(hi * 8 + i + 1) * 16 + j] = (uint16_t)(two >> 16);
   }
   const int row = lane >> 1, ff = fw + 8 * (lane & 1);
   const bool mine = c0 + row < tl.n_valid && ff < p.n_out;
@@ -396,14 +390,14 @@ __device__ __forceinline__ void finish(const Tile& tl, const GemmParams& p, cons
           auto times = [&](const uint4& block) {
             float s[8];
             unpack_block8(block, s);
-            return make_uint4(pack2(v0.x * s[0], v0.y * s[1]), pack2(v0.z * s[2], v0.w * s[3]),
-                              pack2(v1.x * s[4], v1.y * s[5]), pack2(v1.z * s[6], v1.w * s[7]));
+            return make_uint4(pack_bf16x2(v0.x * s[0], v0.y * s[1]), pack_bf16x2(v0.z * s[2], v0.w * s[3]),
+                              pack_bf16x2(v1.x * s[4], v1.y * s[5]), pack_bf16x2(v1.z * s[6], v1.w * s[7]));
           };
           *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out0) + o) = times(in.q[u]);
           *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out1) + o) = times(in.a[u]);
         } else {
           *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out0) + o) =
-              make_uint4(pack2(v0.x, v0.y), pack2(v0.z, v0.w), pack2(v1.x, v1.y), pack2(v1.z, v1.w));
+              make_uint4(pack_bf16x2(v0.x, v0.y), pack_bf16x2(v0.z, v0.w), pack_bf16x2(v1.x, v1.y), pack_bf16x2(v1.z, v1.w));
         }
       }
     }
@@ -498,10 +492,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(B.tfull(a), 1);
-      mbar_init(B.tempty(a), (MODE == kPair ? 2 : 1) * kEpiWarps * 32);
+      mbar_init(B.tempty(a), (MODE == kPair ? 2 : 1) * kEpiWarps);
     }
     mbar_init(B.drain(), 1);
-    mbar_init(B.part_full(), (width > 1 ? width - 1 : 1) * kEpiWarps * 32);
+    mbar_init(B.part_full(), (width > 1 ? width - 1 : 1) * kEpiWarps);
     mbar_init(B.part_free(), (width > 1 ? width - 1 : 1) * kEpiWarps);
     *abort_flag = 0;
     fence_barrier_init();
@@ -643,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (OP == kHidden)
         load_hidden_in(in, p, tl, f0 + quarter * 32,
                        (MODE == kSplit ? rank + set * width : set) * 16, lane);
-      if (!mbar_wait_bounded_warp(B.tfull(acc), acc_phase, abort_flag, p.status)) break;
+      if (!mbar_wait_warp(B.tfull(acc), acc_phase, abort_flag, p.status)) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + (uint32_t)(acc * C::kAccCols);
       const Share sh{rank, width, part};
@@ -660,12 +654,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                               (uint32_t)(slot * kPartChunk + (quarter * 32 + lane) * 4);
           uint32_t r[16];
           tmem_ld_32x32b_x16(taddr + (uint32_t)(g * 16), r);
-          tmem_ld_wait();
+          tmem_ld_wait16(r);
 #pragma unroll
           for (int c = 0; c < 16; ++c) st_cluster_u32(to + (uint32_t)(c * kBM * 4), r[c]);
         }
-        for (int s = 1; s < width; ++s)
-          mbar_arrive_cluster(cluster_addr(B.part_full(), (rank + s) & (width - 1)));
+        __syncwarp();
+        if (lane == 0)
+          for (int s = 1; s < width; ++s)
+            mbar_arrive_cluster(cluster_addr(B.part_full(), (rank + s) & (width - 1)));
         if (!mbar_wait_cluster_warp(B.part_full(), part_phase, abort_flag, p.status)) break;
       }
       epilogue<OP, BN, FT, MODE>(tl, f0, p, d_tmem, quarter, set, lane, st, sh, in);
@@ -676,11 +672,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_cluster(cluster_addr(B.part_free(), (rank + s) & (width - 1)));
       }
       part_phase ^= 1u;
+      // one arrival per warp: the barrier takes arrivals one after another
       tc_fence_before();
-      if constexpr (MODE == kPair)
-        mbar_arrive_cluster(cluster_addr(B.tempty(acc), 0));  // the first CTA issues the MMAs
-      else
-        mbar_arrive(B.tempty(acc));
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(B.tempty(acc), MODE == kPair ? 0 : rank));
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
@@ -699,28 +694,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- host side
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// A bf16 map of the given extents (innermost first), byte strides of the outer dimensions and box.
 bool encode_map(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* extent,
                 const cuuint64_t* stride, const cuuint32_t* box) {
-  static const EncodeTiledFn fn = []() -> EncodeTiledFn {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
-  const cuuint32_t one[4] = {1, 1, 1, 1};
-  return fn != nullptr &&
-         fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), extent,
-            stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return gated_tensor_map(m, ptr, true, rank, extent, stride, box);
 }
 
 // Weights [E, K, n] read MN-major in boxes of 64 features x 64 K rows of one expert.
@@ -888,6 +864,29 @@ bool token_maps(CUtensorMap* l, CUtensorMap* s, const void* ptr, int64_t rows, i
 }
 
 }  // namespace
+
+bool gated_tensor_map(CUtensorMap* m, const void* ptr, bool bf16, int rank, const cuuint64_t* extent,
+                      const cuuint64_t* stride, const cuuint32_t* box) {
+  using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                     const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                     const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                     CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeTiledFn>(f);
+  }();
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn != nullptr &&
+         fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+            (cuuint32_t)rank, const_cast<void*>(ptr), extent, stride, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 cudaError_t enqueue_gated_up_bf16(const GatedFfn& g, void* h, void* saved_a, void* saved_q,
                                   int* status, cudaStream_t stream) {

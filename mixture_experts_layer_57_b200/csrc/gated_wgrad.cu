@@ -4,10 +4,23 @@
 //     dWg[e][i][j] = sum_r dg[r][i] x[r][j],   dWu[e][i][j] = sum_r du[r][i] x[r][j]
 // in one persistent launch over the output tiles of all three. Both operands are read MN-major
 // from the row-major activations (TMA boxes of 64 columns x 64 rows, 128-byte swizzle; no
-// transposed copies). The last K block of a segment also holds rows of the next expert, whose
-// values may be anything: the rows past the segment, up to the next multiple of 16, are cleared
-// in shared memory and only the MMAs (K = 16 each) that cover the segment are issued. Experts
-// without rows get zeros.
+// transposed copies).
+//
+// With some 100 rows an expert the sums are short and writing the gradients bounds the kernel.
+// A pair of CTAs computes a 256 x 256 tile (cta_group::2, 128 rows of it in each), so a tile costs
+// each CTA 32 KB of loads per 64 rows; gradients leave through shared memory as TMA stores of whole
+// 128-byte lines, two in flight per warp, while the next tile's MMAs run into a second accumulator.
+// 128 experts of 128 rows, d 1024, f 4096: 964 us (3.7 GB at 3.8 TB/s; 870 with every tile written
+// to one place, 680 without the stores: what is left is the MMAs of two blocks a tile and their
+// hand-overs). One CTA a tile and rows written through fp32 staging: 1050 us. 16 epilogue warps with
+// one buffer: 947, but 14% slower where the products bound (8 experts, d 4096, f 14336: 3.4 ms).
+//
+// The last K block of a segment is loaded in boxes of 16 rows, the last of which may also hold rows
+// of the next expert, whose values may be anything: each CTA clears its own in shared memory before
+// the MMAs (K = 16 each). A warp of its own does that as soon as such a tail has landed (its loads
+// count on a barrier of their own CTA, those of other blocks on the first CTA's), long before the
+// MMAs of the blocks before are issued, and reports to the first CTA's `tail` barrier.
+// Experts without rows get zeros.
 #include "common.cuh"
 #include "gated.cuh"
 #include "kernels.h"
@@ -15,32 +28,36 @@
 namespace moe {
 namespace {
 
-constexpr int kBM = 128;
-constexpr int kBN = 256;
+constexpr int kTile = 256;       // rows and columns of a pair's output tile
+constexpr int kHalf = 128;       // A columns (tile rows) and B columns that one CTA loads
 constexpr int kBK = 64;          // rows per stage
 constexpr int kUmmaK = 16;
-constexpr int kThreads = 320;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiSets = 2;     // epilogue warps for each quarter of a CTA's rows
+constexpr int kEpiWarps = 4 * kEpiSets;
+constexpr int kThreads = 96 + 32 * kEpiWarps;  // TMA, MMA, tails, epilogue
 constexpr int kBoxBytes = 64 * kBK * 2;  // one 64 x 64 bf16 box
-constexpr int kEpiRowFloats = 36;        // 32 columns + 4 pad (16-byte aligned rows)
-constexpr int kABytes = kBM * kBK * 2;
-constexpr int kStageBytes = kABytes + kBN * kBK * 2;
-constexpr int kEpiStageBytes = kEpiWarps * 32 * kEpiRowFloats * 4;
-constexpr int kStages = (200 * 1024 - kEpiStageBytes) / kStageBytes;
-constexpr int kTmemCols = 2 * kBN;
+constexpr int kABytes = kHalf * kBK * 2;
+constexpr int kStageBytes = 2 * kABytes;
+constexpr int kOutBytes = 32 * 128;      // 32 tile rows of one 128-byte line each
+constexpr int kEpiBytes = kEpiWarps * 2 * kOutBytes;
+constexpr int kStages = 5;
+constexpr int kGroup = 8;               // rows of tiles walked together
+constexpr int kTmemCols = 2 * kTile;
 constexpr int kBarBytes = 8 * 32;
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiStageBytes + kBarBytes + 16;
-static_assert(2 * kStages + 5 <= 32, "barrier area too small");
+constexpr int kSmemBytes =
+    1024 + kStages * kStageBytes + kEpiBytes + kBarBytes + 16;
+static_assert(4 * kStages + 5 <= 32, "barrier area too small");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 
 struct WgradMaps {
-  CUtensorMap dy, h, dg, du, x;
+  CUtensorMap a[3], b[2];    // dy, dg, du; h, x: boxes of 64 rows
+  CUtensorMap ta[3], tb[2];  // the same in boxes of 16 rows
+  CUtensorMap out[3];        // dWd, dWg, dWu
 };
 struct WgradParams {
   const int32_t* offsets;
   int E, d, f;
   int64_t rows_max;
-  void *dw_down, *dw_gate, *dw_up;
   int out_bf16;
   int* status;
 };
@@ -51,35 +68,74 @@ struct WTile {
   int which, e, m0, n0, M, N, row0, rows;
 };
 
-__device__ __forceinline__ WTile decode(int t, const WgradParams& p, int t_down, int t_up) {
-  WTile w;
-  const int per_e = t_down + 2 * t_up;
-  w.e = t / per_e;
-  int u = t - w.e * per_e;
-  int nt;
-  if (u < t_down) {
+// The tiles of one pair: every `step`-th from `first` on. An expert's tiles are those of dWd, then
+// those of dWg and dWu by turns (both read the same x columns); of a problem, kGroup rows of tiles
+// at a time go column by column, so that the pairs at work share columns of both operands in L2.
+// With short sums a tile is a microsecond's work: divisions are by multiplication and the segment's
+// ends are kept while the expert stays.
+struct Walk {
+  int e = 0, step, row0 = 0, rows = 0;
+  unsigned u, td, tf, per;  // u: tile within the expert; tiles along d and f and their product
+  __device__ __forceinline__ Walk(const WgradParams& p, int first, int s) : step(s), u(first) {
+    td = (unsigned)(p.d + kTile - 1) / kTile;
+    tf = (unsigned)(p.f + kTile - 1) / kTile;
+    per = td * tf;
+    e = -1;
+    u += 3 * per;  // settle() steps into expert 0
+    settle(p);
+  }
+  __device__ __forceinline__ void settle(const WgradParams& p) {
+    if (u < 3 * per) return;
+    while (u >= 3 * per) {
+      u -= 3 * per;
+      ++e;
+    }
+    if (e < p.E) {
+      int a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
+      if (a < 0 || b < a || (int64_t)b > p.rows_max) a = b = 0;  // invalid: treated as empty
+      row0 = a;
+      rows = b - a;
+    }
+  }
+  __device__ __forceinline__ bool valid(const WgradParams& p) const { return e < p.E; }
+  __device__ __forceinline__ void next(const WgradParams& p) {
+    u += step;
+    settle(p);
+  }
+  __device__ __forceinline__ WTile tile(const WgradParams& p) const {
+    WTile w;
+    w.e = e;
+    w.row0 = row0;
+    w.rows = rows;
+    unsigned v = u, mt = td, nt = tf;
     w.which = 0;
     w.M = p.d;
     w.N = p.f;
-    nt = (p.f + kBN - 1) / kBN;
-  } else {
-    // the gate's and the up projection's tiles alternate: both read the same x columns
-    u -= t_down;
-    w.which = 1 + (u & 1);
-    u >>= 1;
-    w.M = p.f;
-    w.N = p.d;
-    nt = (p.d + kBN - 1) / kBN;
+    if (u >= per) {
+      v = u - per;
+      w.which = 1 + (int)(v & 1u);
+      v >>= 1;
+      w.M = p.f;
+      w.N = p.d;
+      mt = tf;
+      nt = td;
+    }
+    // v < 2^13 (d, f <= 16384): exact
+    const unsigned band = kGroup * nt, g = div_small(v, band);
+    v -= g * band;
+    const unsigned high = min((unsigned)kGroup, mt - g * kGroup), n = div_small(v, high);
+    w.m0 = (int)(g * kGroup + v - n * high) * kTile;
+    w.n0 = (int)n * kTile;
+    return w;
   }
-  const int mt = u / nt;
-  w.m0 = mt * kBM;
-  w.n0 = (u - mt * nt) * kBN;
-  int a = p.offsets[w.e], b = p.offsets[w.e + 1];
-  if (a < 0 || b < a || (int64_t)b > p.rows_max) a = b = 0;  // invalid: treated as empty
-  w.row0 = a;
-  w.rows = b - a;
-  return w;
-}
+  // v / by for v below 2^20: a float quotient, whose error is under one step, put right
+  static __device__ __forceinline__ unsigned div_small(unsigned v, unsigned by) {
+    unsigned q = (unsigned)__fdividef((float)v, (float)by);
+    if (q * by > v) --q;
+    if ((q + 1) * by <= v) ++q;
+    return q;
+  }
+};
 
 __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, int* status) {
   const uint64_t t0 = global_timer_ns();
@@ -91,39 +147,69 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, int* s
   }
 }
 
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+// Whether a K block with `left` rows of its segment to go holds rows to clear.
+__device__ __forceinline__ bool has_tail(int left) { return left < kBK && (left & (kUmmaK - 1)) != 0; }
+
+// The uses of each stage by whole blocks and by tails, which count on different barriers: next()
+// gives the parity of the next one's phase, last() that of the last one's.
+struct Uses {
+  uint32_t phase[2] = {0, 0}, any[2] = {0, 0};  // bits: stages
+  __device__ __forceinline__ uint32_t next(int stage, bool tail) {
+    const uint32_t parity = phase[tail] >> stage & 1u;
+    phase[tail] ^= 1u << stage;
+    any[tail] |= 1u << stage;
+    return parity;
+  }
+  __device__ __forceinline__ uint32_t last(int stage, bool tail) const {
+    return (phase[tail] >> stage & 1u) ^ 1u;
+  }
+};
+
+// Clears this CTA's stage rows from `valid` to the next multiple of 16 (whole warp). A row of an
+// MN-major box is 128 contiguous bytes; the swizzle permutes 16-byte chunks inside it.
+__device__ __forceinline__ void clear_tail(uint8_t* stage, int valid, int lane) {
+  const int chunks = (kUmmaK - valid % kUmmaK) * 8;
+#pragma unroll
+  for (int bx = 0; bx < kStageBytes / kBoxBytes; ++bx)
+    for (int c = lane; c < chunks; c += 32)
+      *reinterpret_cast<uint4*>(stage + bx * kBoxBytes + valid * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  __syncwarp();
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     gated_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t base_addr = (raw_addr + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (base_addr - raw_addr);
-  float* epi_stage = reinterpret_cast<float*>(base + kStages * kStageBytes);
-  uint8_t* aux = base + kStages * kStageBytes + kEpiStageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(aux);
+  uint8_t* aux = base + kStages * kStageBytes + kEpiBytes;
+  const uint32_t bars = smem_u32(aux);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(aux + kBarBytes);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(aux + kBarBytes + 4);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
   constexpr int S = kStages;
-  auto full_bar = [&](int s) { return smem_u32(&bars[s]); };
-  auto empty_bar = [&](int s) { return smem_u32(&bars[S + s]); };
-  auto tfull_bar = [&](int a) { return smem_u32(&bars[2 * S + a]); };
-  auto tempty_bar = [&](int a) { return smem_u32(&bars[2 * S + 2 + a]); };
-  const uint32_t drain_bar = smem_u32(&bars[2 * S + 4]);
+  auto full_bar = [&](int s) { return bars + 8u * s; };  // of the first CTA: both CTAs' loads
+  auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
+  auto landed_bar = [&](int s) { return bars + 8u * (2 * S + s); };  // this CTA's loads of a tail
+  auto tail_bar = [&](int s) { return bars + 8u * (3 * S + s); };  // of the first CTA: both cleared
+  auto tfull_bar = [&](int a) { return bars + 8u * (4 * S + a); };
+  auto tempty_bar = [&](int a) { return bars + 8u * (4 * S + 2 + a); };  // of the first CTA
+  const uint32_t drain_bar = bars + 8u * (4 * S + 4);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
+      mbar_init(landed_bar(s), 1);
+      mbar_init(tail_bar(s), 2);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), kEpiWarps * 32);
+      mbar_init(tempty_bar(a), 2 * kEpiWarps);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -131,184 +217,205 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_holder), kTmemCols);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(tmem_holder), kTmemCols);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  const int t_down = ((p.d + kBM - 1) / kBM) * ((p.f + kBN - 1) / kBN);
-  const int t_up = ((p.f + kBM - 1) / kBM) * ((p.d + kBN - 1) / kBN);
-  const int total = p.E * (t_down + 2 * t_up);
+  const int first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
 
   if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
     if (lane == 0) {
-      int stage = 0, issued = 0;
+      int stage = 0;
       uint32_t phase = 0;
+      Uses uses;
       bool ok = true;
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        const WTile w = decode(t, p, t_down, t_up);
-        const CUtensorMap* ma = w.which == 0 ? &maps.dy : (w.which == 1 ? &maps.dg : &maps.du);
-        const CUtensorMap* mb = w.which == 0 ? &maps.h : &maps.x;
+      for (Walk walk(p, first, step); walk.valid(p) && ok; walk.next(p)) {
+        const WTile w = walk.tile(p);
+        const int bi = w.which == 0 ? 0 : 1;
+        const int m0 = w.m0 + rank * kHalf, n0 = w.n0 + rank * kHalf;
         for (int r = 0; r < w.rows; r += kBK) {
           if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.status)) {
             ok = false;
             break;
           }
           const uint32_t sa = base_addr + stage * kStageBytes;
-          mbar_arrive_expect_tx(full_bar(stage), kStageBytes);
+          const int valid = w.rows - r;
+          const uint32_t bytes = valid >= kBK ? kStageBytes : (uint32_t)(valid + 15) / 16 * 16 * 2 * kHalf * 2;
+          const bool tail = has_tail(valid);
+          const uint32_t bar = tail ? landed_bar(stage) : full_bar(stage);
+          const uint32_t count_on = cluster_addr(bar, tail ? rank : 0);
+          if (tail || rank == 0) mbar_arrive_expect_tx(bar, tail ? bytes : 2 * bytes);
+          uses.next(stage, tail);
+          const int rows16 = valid >= kBK ? 0 : (valid + 15) / 16;
 #pragma unroll
-          for (int j = 0; j < kBM / 64; ++j)
-            tma_load_2d(sa + j * kBoxBytes, ma, w.m0 + 64 * j, w.row0 + r, full_bar(stage));
-#pragma unroll
-          for (int j = 0; j < kBN / 64; ++j)
-            tma_load_2d(sa + kABytes + j * kBoxBytes, mb, w.n0 + 64 * j, w.row0 + r,
-                        full_bar(stage));
-          ++issued;
+          for (int j = 0; j < kHalf / 64; ++j) {
+            const uint32_t da = sa + j * kBoxBytes, db = sa + kABytes + j * kBoxBytes;
+            if (rows16 == 0) {
+              tma_load_2d_pair(da, &maps.a[w.which], m0 + 64 * j, w.row0 + r, count_on);
+              tma_load_2d_pair(db, &maps.b[bi], n0 + 64 * j, w.row0 + r, count_on);
+            } else {
+#pragma unroll 1
+              for (int i = 0; i < rows16; ++i) {
+                tma_load_2d_pair(da + i * 2048, &maps.ta[w.which], m0 + 64 * j, w.row0 + r + 16 * i, count_on);
+                tma_load_2d_pair(db + i * 2048, &maps.tb[bi], n0 + 64 * j, w.row0 + r + 16 * i, count_on);
+              }
+            }
+          }
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      for (int i = max(0, issued - S); i < issued; ++i)
-        wait_drain(full_bar(i % S), (uint32_t)((i / S) & 1), p.status);
+      // drain: the loads of the last uses may still be landing
+      for (int s = 0; s < S; ++s) {
+        if (rank == 0 && uses.any[0] >> s & 1u) wait_drain(full_bar(s), uses.last(s, false), p.status);
+        if (uses.any[1] >> s & 1u) wait_drain(landed_bar(s), uses.last(s, true), p.status);
+      }
     }
   } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA issuer (whole warp)
-    int stage = 0, acc = 0;
-    uint32_t phase = 0, acc_phase = 0;
-    bool ok = true;
-    const uint32_t idesc = idesc_bf16_f32_major(kBM, kBN, true, true);
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const WTile w = decode(t, p, t_down, t_up);
-      if (!mbar_wait_bounded_warp(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.status)) break;
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kBN);
-      for (int r = 0; r < w.rows; r += kBK) {
-        if (!mbar_wait_bounded_warp(full_bar(stage), phase, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0 && rank == 0) {
+      int stage = 0, acc = 0;
+      uint32_t acc_phase = 0;
+      Uses uses;
+      bool ok = true;
+      const uint32_t idesc = idesc_bf16_f32_major(kTile, kTile, true, true);
+      for (Walk walk(p, first, step); walk.valid(p) && ok; walk.next(p)) {
+        if (!mbar_wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.status)) break;
         tc_fence_after();
-        const uint32_t sa = base_addr + stage * kStageBytes;
-        const int valid = min(kBK, w.rows - r);
-        const int kend = (valid + kUmmaK - 1) & ~(kUmmaK - 1);
-        if (valid < kend) {
-          // a row of an MN-major box is 128 contiguous bytes; the swizzle permutes 16-byte
-          // chunks inside it
-          uint8_t* sp = base + stage * kStageBytes;
-          const int chunks = (kend - valid) * 8;
-          for (int i = lane; i < (kBM + kBN) / 64 * chunks; i += 32) {
-            const int bx = i / chunks, c = i - bx * chunks;
-            *reinterpret_cast<uint4*>(sp + bx * kBoxBytes + valid * 128 + c * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) {
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kTile);
+        for (int left = walk.rows; left > 0; left -= kBK) {
+          const bool tail = has_tail(left);
+          const uint32_t parity = uses.next(stage, tail);
+          ok = tail ? mbar_wait_cluster(tail_bar(stage), parity, abort_flag, p.status)
+                    : mbar_wait_bounded(full_bar(stage), parity, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sa = base_addr + stage * kStageBytes;
           const uint64_t adesc = smem_desc_sw128_mn(sa);
           const uint64_t bdesc = smem_desc_sw128_mn(sa + kABytes);
-          for (int kk = 0; kk < kend / kUmmaK; ++kk)
-            tc_mma_bf16(d_tmem, adesc + (uint64_t)(kk * (kMnKStepBytes >> 4)),
-                        bdesc + (uint64_t)(kk * (kMnKStepBytes >> 4)), idesc,
-                        (r | kk) != 0 ? 1u : 0u);
-          tc_commit(empty_bar(stage));
+#pragma unroll
+          for (int kk = 0; kk < kBK / kUmmaK; ++kk)
+            if (kk * kUmmaK < left)
+              tc_mma_bf16_pair(d_tmem, adesc + (uint64_t)(kk * (kMnKStepBytes >> 4)),
+                               bdesc + (uint64_t)(kk * (kMnKStepBytes >> 4)), idesc,
+                               left != walk.rows || kk != 0 ? 1u : 0u);
+          tc_commit_pair_both(empty_bar(stage), cluster_addr(empty_bar(stage), 1));
+          if (++stage == S) stage = 0;
         }
-        __syncwarp();
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        if (!ok) break;
+        tc_commit_pair_both(tfull_bar(acc), cluster_addr(tfull_bar(acc), 1));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
       }
-      if (!ok) break;
-      if (lane == 0) tc_commit(tfull_bar(acc));
-      __syncwarp();
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
-    }
-    if (lane == 0) {
-      tc_commit(drain_bar);
+      tc_commit_pair_local(drain_bar);
       wait_drain(drain_bar, 0, p.status);
     }
     __syncwarp();
-  } else {
-    // ---------------------------------------------------------- epilogue (warps 2..9)
-    const int quarter = warp & 3;
-    const int half = (warp - 2) >> 2;
-    float* st = epi_stage + (warp - 2) * 32 * kEpiRowFloats;
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
-      const WTile w = decode(t, p, t_down, t_up);
-      const bool empty = w.rows == 0;  // nothing was accumulated: the tile is zero
-      uint8_t* out = reinterpret_cast<uint8_t*>(
-          w.which == 0 ? p.dw_down : (w.which == 1 ? p.dw_gate : p.dw_up));
-      if (!mbar_wait_bounded_warp(tfull_bar(acc), acc_phase, abort_flag, p.status)) break;
-      tc_fence_after();
-      const int mw = w.m0 + quarter * 32;  // first row of this warp
-      const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kBN);
-      for (int c0 = half * 32; c0 < kBN; c0 += 64) {
-        uint32_t r0[16], r1[16];
-        tmem_ld_32x32b_x16(taddr + (uint32_t)c0, r0);
-        tmem_ld_32x32b_x16(taddr + (uint32_t)c0 + 16, r1);
-        tmem_ld_wait();
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint32_t* r = q < 4 ? r0 : r1;
-          const int o = 4 * (q & 3);
-          *reinterpret_cast<float4*>(st + lane * kEpiRowFloats + 4 * q) =
-              empty ? make_float4(0.f, 0.f, 0.f, 0.f)
-                    : make_float4(__uint_as_float(r[o]), __uint_as_float(r[o + 1]),
-                                  __uint_as_float(r[o + 2]), __uint_as_float(r[o + 3]));
+  } else if (warp == 2) {
+    // ---------------------------------------------------------- tails
+    int stage = 0;
+    Uses uses;
+    bool ok = true;
+    for (Walk walk(p, first, step); walk.valid(p) && ok; walk.next(p)) {
+      for (int left = walk.rows; left > 0; left -= kBK) {
+        if (has_tail(left)) {
+          ok = mbar_wait_warp(landed_bar(stage), uses.next(stage, true), abort_flag, p.status);
+          if (!ok) break;
+          clear_tail(base + stage * kStageBytes, left, lane);
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(tail_bar(stage), 0));
         }
+        if (++stage == S) stage = 0;
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue
+    // this warp's 32 tile rows, every kEpiSets-th line of 128 bytes: each lane writes its row's 128
+    // bytes into one of the warp's buffers, and one lane stores that
+    const int quarter = warp & 3;
+    const int set = (warp - 3) >> 2;
+    const int cols = p.out_bf16 ? 64 : 32;  // of a line
+    const int buf0 = kStages * kStageBytes + (warp - 3) * 2 * kOutBytes;
+    int acc = 0, buf = 0;
+    uint32_t acc_phase = 0;
+    for (Walk walk(p, first, step); walk.valid(p); walk.next(p)) {
+      const WTile w = walk.tile(p);
+      const bool empty = w.rows == 0;  // nothing was accumulated: the tile is zero
+      const int m = w.m0 + rank * kHalf + quarter * 32;  // first row of this warp
+      if (!mbar_wait_warp(tfull_bar(acc), acc_phase, abort_flag, p.status)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kTile);
+      const int n_end = m < w.M ? min(kTile, w.N - w.n0) : 0;
+      // the accumulator is free once this warp has read its last columns; one arrival per warp, as
+      // the barrier takes arrivals one after another
+      auto release = [&]() {
+        tc_fence_before();
         __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty_bar(acc), 0));
+      };
+      if (set * cols >= n_end) release();
+#pragma unroll 1
+      for (int c0 = set * cols; c0 < n_end; c0 += kEpiSets * cols) {
+        uint32_t line[32];
         if (p.out_bf16) {
-          const int n = w.n0 + c0 + 8 * (lane & 3);
+          uint32_t r[4][16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = 8 * i + (lane >> 2);
-            const int m = mw + rr;
-            if (m < w.M && n < w.N) {
-              const float4 v0 = *reinterpret_cast<const float4*>(st + rr * kEpiRowFloats + 8 * (lane & 3));
-              const float4 v1 = *reinterpret_cast<const float4*>(st + rr * kEpiRowFloats + 8 * (lane & 3) + 4);
-              uint4 v;
-              v.x = (uint32_t)f32_to_bf16_rn(v0.x) | ((uint32_t)f32_to_bf16_rn(v0.y) << 16);
-              v.y = (uint32_t)f32_to_bf16_rn(v0.z) | ((uint32_t)f32_to_bf16_rn(v0.w) << 16);
-              v.z = (uint32_t)f32_to_bf16_rn(v1.x) | ((uint32_t)f32_to_bf16_rn(v1.y) << 16);
-              v.w = (uint32_t)f32_to_bf16_rn(v1.z) | ((uint32_t)f32_to_bf16_rn(v1.w) << 16);
-              *reinterpret_cast<uint4*>(out + 2 * (((int64_t)w.e * w.M + m) * w.N + n)) = v;
-            }
+          for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x16(taddr + (uint32_t)(c0 + 16 * q), r[q]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld_wait16(r[q]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              line[8 * q + i] = pack_bf16x2(__uint_as_float(r[q][2 * i]), __uint_as_float(r[q][2 * i + 1]));
           }
         } else {
-          const int n = w.n0 + c0 + 4 * (lane & 7);
+          uint32_t r[2][16];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rr = 4 * i + (lane >> 3);
-            const int m = mw + rr;
-            if (m < w.M && n < w.N)
-              *reinterpret_cast<float4*>(out + 4 * (((int64_t)w.e * w.M + m) * w.N + n)) =
-                  *reinterpret_cast<const float4*>(st + rr * kEpiRowFloats + 4 * (lane & 7));
+          for (int q = 0; q < 2; ++q) tmem_ld_32x32b_x16(taddr + (uint32_t)(c0 + 16 * q), r[q]);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            tmem_ld_wait16(r[q]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) line[16 * q + i] = r[q][i];
           }
         }
+        if (c0 + kEpiSets * cols >= n_end) release();
+        if (lane == 0) bulk_wait_read<1>();  // the buffer's last store has read it
         __syncwarp();
+        uint8_t* row = base + buf0 + buf * kOutBytes + lane * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(row + ((c ^ (lane & 7)) << 4)) =
+              empty ? make_uint4(0u, 0u, 0u, 0u)
+                    : make_uint4(line[4 * c], line[4 * c + 1], line[4 * c + 2], line[4 * c + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&maps.out[w.which], base_addr + buf0 + buf * kOutBytes, w.n0 + c0, m, w.e);
+          bulk_commit();
+        }
+        buf ^= 1;
       }
-      tc_fence_before();
-      mbar_arrive(tempty_bar(acc));
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
 
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  cluster_sync();  // no commit or arrive targets the other CTA after this
   pdl_trigger();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, kTmemCols);
+    tmem_dealloc_pair(tmem_base, kTmemCols);
   }
 }
 
@@ -440,19 +547,29 @@ cudaError_t enqueue_gated_weight_grad_bf16(const GatedFfn& g, const void* dy, co
                                            void* dw_gate, void* dw_up, bool grad_bf16, int* status,
                                            cudaStream_t stream) {
   WgradMaps m;
-  if (!make_bf16_map_2d(&m.dy, dy, g.rows_max, g.d, 64, kBK) ||
-      !make_bf16_map_2d(&m.h, h, g.rows_max, g.f, 64, kBK) ||
-      !make_bf16_map_2d(&m.dg, dg, g.rows_max, g.f, 64, kBK) ||
-      !make_bf16_map_2d(&m.du, du, g.rows_max, g.f, 64, kBK) ||
-      !make_bf16_map_2d(&m.x, g.x, g.rows_max, g.d, 64, kBK))
+  // gradients [E, M, N], stored in boxes of 32 rows of one 128-byte line
+  auto grad_map = [&](CUtensorMap* map, const void* ptr, int M, int N) {
+    const cuuint64_t size = grad_bf16 ? 2 : 4;
+    const cuuint64_t extent[3] = {(cuuint64_t)N, (cuuint64_t)M, (cuuint64_t)g.E};
+    const cuuint64_t stride[2] = {N * size, (cuuint64_t)M * N * size};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / size), 32, 1};
+    return gated_tensor_map(map, ptr, grad_bf16, 3, extent, stride, box);
+  };
+  const void* acts[5] = {dy, dg, du, h, g.x};
+  const int cols[5] = {g.d, g.f, g.f, g.f, g.d};
+  for (int i = 0; i < 5; ++i)
+    if (!make_bf16_map_2d(i < 3 ? &m.a[i] : &m.b[i - 3], acts[i], g.rows_max, cols[i], 64, kBK) ||
+        !make_bf16_map_2d(i < 3 ? &m.ta[i] : &m.tb[i - 3], acts[i], g.rows_max, cols[i], 64, 16))
+      return cudaErrorInvalidValue;
+  if (!grad_map(&m.out[0], dw_down, g.d, g.f) || !grad_map(&m.out[1], dw_gate, g.f, g.d) ||
+      !grad_map(&m.out[2], dw_up, g.f, g.d))
     return cudaErrorInvalidValue;
-  WgradParams p{g.offsets, g.E, g.d, g.f, g.rows_max, dw_down, dw_gate, dw_up, grad_bf16 ? 1 : 0,
-                status};
+  const WgradParams p{g.offsets, g.E, g.d, g.f, g.rows_max, grad_bf16 ? 1 : 0, status};
   static int attr_done[64] = {0};  // per device
   const cudaError_t e = ensure_dynamic_smem(gated_wgrad_kernel, kSmemBytes, attr_done);
   if (e != cudaSuccess) return e;
-  return launch_kernel(gated_wgrad_kernel, dim3(num_sms()), dim3(kThreads), kSmemBytes, stream, m,
-                       p);
+  return launch_kernel(gated_wgrad_kernel, dim3(num_sms() / 2 * 2), dim3(kThreads), kSmemBytes, stream,
+                       m, p);
 }
 
 }  // namespace moe
