@@ -421,8 +421,10 @@ moe_status moe_layer_backward(const moe_layer_args* args, const void* d_out, flo
  * within [0, rows_max] set MOE_DEVERR_BAD_OFFSETS. capacity_hint: an upper bound on the rows of
  * any one expert (normally C); it selects tile sizes and how sums are split, so it may change
  * results in their rounding, and is otherwise free to be wrong.
- * Limits: those of moe_expert_ffn (bf16: d_model and d_ff multiples of 8). bf16 runs on tcgen05
- * tensor cores (fp32 accumulate), fp32 on fp32 FMA (no TF32). */
+ * Limits: those of moe_expert_ffn (bf16: d_model and d_ff multiples of 8). Both types run on tcgen05
+ * tensor cores and accumulate in fp32. fp32 factors are split in two tf32 parts each, which keeps
+ * sums as exact as fp32 FMAs' (products within 2^-20, 2^-23 on average); there an infinite factor
+ * makes its sums NaN. */
 typedef enum { MOE_GATE_SILU = 0, MOE_GATE_GELU = 1 } moe_gate_act;
 typedef struct {
   const void* x_packed;

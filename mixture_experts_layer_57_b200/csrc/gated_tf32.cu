@@ -1,0 +1,604 @@
+// The gated expert FFN (forward and backward) of fp32 layers on sm_100a tensor cores.
+//
+//     up      h[r, i]  = act(zg) * zu,  zg = Wg[e][i] . x[r] + bg,  zu = Wu[e][i] . x[r] + bu
+//     down    y[r, :]  = Wd[e] h[r, :] + bd
+//     hidden  dh[r, i] = sum_m dy[r, m] Wd[e][m, i],  du = dh act(zg),  dg = dh zu act'(zg)
+//     input   dx[r, :] = Wg[e]^T dg[r, :] + Wu[e]^T du[r, :]
+//     weight  dWd[e] = dy^T h,  dWg[e] = dg^T x,  dWu[e] = du^T x   (sums over the rows of e)
+//
+// Sums as exact as fp32 arithmetic's. Every factor is split in two tf32 numbers, hi = x cut to 11
+// bits and lo = x - hi rounded to 11, together within 2^-22 of x, and a product is hi hi + hi lo +
+// lo hi: lo lo, which is left out, is 2^-20 of it at most and 2^-23 on average. The tensor cores cut
+// each sum towards zero instead of rounding it (measured: 31 additions of 1.94 2^-24 to 1 leave 1),
+// which over a long sum would cost several bits. So hi hi and the other two, 2^-10 of it, have
+// accumulators of their own, 64 of K are summed in TMEM at a time, and the epilogue warps add those
+// sums in registers, rounded to nearest. Measured against 64 bits, relative to the whole output
+// (1000 rows, d 501, f 1334): 7e-7, where fp32 FMAs in index order gave 9e-7.
+//
+// Operands have any width, so rows start on any multiple of 4 bytes, which no TMA copy can do: eight
+// warps load them (the next block's while they split this one's), split, and write both parts
+// K-major in the swizzled layout of the MMA. The lanes of the accumulator are the output's
+// contiguous index, so stores go out as whole lines. Tiles are 128 x 128, or 128 x 64 where the
+// former are fewer than the SMs. What bounds it: the loads and splits, some 3000 cycles for 32 of K
+// (three tf32 MMA passes: 768). 4 experts, 1000 rows, d 501, f 1334: up 68 us, down 63 (tiles of
+// fp32 FMAs: 123 and 115).
+#include <algorithm>
+
+#include "common.cuh"
+#include "gated.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+enum Op { kUp = 0, kDown = 1, kHidden = 2, kInput = 3, kWeight = 4 };
+
+constexpr int kBM = 128, kBN = 128;
+constexpr int kBK = 32;                  // fp32 of K per stage: one 128-byte swizzle row
+constexpr int kChunk = 2;                // K blocks per sum in TMEM
+constexpr int kStages = 3;
+constexpr int kPartBytes = kBM * kBK * 4;        // one part (hi or lo) of one operand
+constexpr int kStageBytes = 4 * kPartBytes;      // A hi, A lo, B hi, B lo
+constexpr int kLoadWarps = 8, kEpiWarps = 8;
+// One warp of MMAs: 17 warps, for which the register file leaves 96 a thread.
+constexpr int kThreads = 32 * (kLoadWarps + 1 + kEpiWarps);
+constexpr int kAccCols = 2 * kBN;        // hi hi, and the small products
+constexpr int kTmemCols = 2 * kAccCols;  // two of both
+constexpr int kBarBytes = 8 * 16;
+constexpr int kSmemBytes =
+    1024 + kStages * kStageBytes + kBarBytes + 16 + 2 * 4 * (MOE_MAX_EXPERTS + 1);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+
+struct Args {
+  const int32_t* offsets;
+  int E, act, bn;
+  int64_t rows_max;
+  int n_out;                 // output features (kWeight: unused)
+  int K;                     // of each product (kWeight: unused, the segment's rows)
+  int d, f;
+  const float *a0, *a1;      // weights; kWeight: h, x
+  const float *b0, *b1, *b2; // token rows; kWeight: dy, dg, du
+  const float *bias0, *bias1;
+  const float *in0, *in1;    // kHidden: act(zg), zu act'(zg)
+  float *out0, *out1, *out2;
+  int* status;
+};
+
+// A tile: lanes are output features f0.., columns token rows row0.. (kWeight: rows row0.. of the
+// gradient `which`), n_valid of them, of expert e; n_out features, sums over K (twice for kInput).
+struct Tile {
+  int e, f0, row0, n_valid, which, n_out, K, seg;
+};
+
+template <int OP>
+__device__ __forceinline__ int tile_count(const Args& p, const int* prefix) {
+  if constexpr (OP != kWeight) return prefix[p.E];
+  const int t0 = ((p.f + kBM - 1) / kBM) * ((p.d + p.bn - 1) / p.bn);
+  const int t1 = ((p.d + kBM - 1) / kBM) * ((p.f + p.bn - 1) / p.bn);
+  return p.E * (t0 + 2 * t1);
+}
+
+template <int OP>
+__device__ __forceinline__ Tile tile_at(const Args& p, int t, const int* prefix, const int* seg) {
+  Tile w;
+  if constexpr (OP == kWeight) {
+    // dWd [d, f], then dWg and dWu [f, d]: features are a gradient row's elements
+    const int t0 = ((p.f + kBM - 1) / kBM) * ((p.d + p.bn - 1) / p.bn);
+    const int t1 = ((p.d + kBM - 1) / kBM) * ((p.f + p.bn - 1) / p.bn);
+    w.e = t / (t0 + 2 * t1);
+    int u = t - w.e * (t0 + 2 * t1);
+    w.which = u < t0 ? 0 : 1 + (u - t0) / t1;
+    if (w.which != 0) u = (u - t0) % t1;
+    w.n_out = w.which == 0 ? p.f : p.d;
+    const int rows = w.which == 0 ? p.d : p.f;
+    const int nt = (rows + p.bn - 1) / p.bn;
+    w.f0 = u / nt * kBM;
+    w.row0 = u % nt * p.bn;
+    w.n_valid = min(p.bn, rows - w.row0);
+    int a = __ldg(p.offsets + w.e), b = __ldg(p.offsets + w.e + 1);
+    if (a < 0 || b < a || (int64_t)b > p.rows_max) a = b = 0;  // flagged by the passes before
+    w.seg = a;
+    w.K = b - a;
+  } else {
+    int lo = 0, hi = p.E;  // prefix[lo] <= t < prefix[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    const int rows = seg[lo + 1] - seg[lo], ntt = (rows + p.bn - 1) / p.bn;
+    const int local = t - prefix[lo], ft = local / ntt, jt = local - ft * ntt;
+    w.e = lo;
+    w.f0 = ft * (OP == kUp ? kBM / 2 : kBM);
+    w.row0 = seg[lo] + jt * p.bn;
+    w.n_valid = min(p.bn, rows - jt * p.bn);
+    w.which = 0;
+    w.n_out = p.n_out;
+    w.K = p.K;
+    w.seg = 0;
+  }
+  return w;
+}
+
+template <int OP>
+__device__ __forceinline__ int k_blocks(const Tile& w) {
+  return (OP == kInput ? 2 : 1) * ((w.K + kBK - 1) / kBK);
+}
+
+// One warp: seg[e] and the first tile of every expert; none if the offsets are not non-decreasing
+// within [0, rows_max], which is flagged.
+__device__ __forceinline__ void build_tile_list(const Args& p, int n_ftiles, int* prefix, int* seg,
+                                                int lane) {
+  int run = 0;
+  bool bad = false;
+  for (int e0 = 0; e0 < p.E; e0 += 32) {
+    const int e = e0 + lane;
+    int tiles = 0;
+    if (e < p.E) {
+      const int a = p.offsets[e], b = p.offsets[e + 1];
+      seg[e] = a;
+      if (a < 0 || b < a || (int64_t)b > p.rows_max) bad = true;
+      else tiles = n_ftiles * ((b - a + p.bn - 1) / p.bn);
+    }
+    int incl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (e < p.E) prefix[e] = run + incl - tiles;
+    run += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  if (lane == 0) {
+    seg[p.E] = p.offsets[p.E];
+    prefix[p.E] = bad ? 0 : run;
+    if (bad && blockIdx.x == 0) set_device_error(p.status, MOE_DEVERR_BAD_OFFSETS);
+  }
+}
+
+// How a load thread's 16 elements of one operand's K block lie: four units of four neighbours along
+// k, 16 bytes of the stage each.
+//   kWide    rows are contiguous along k and start on 16 bytes: a load per unit, eight lanes to a
+//            row, 32 rows from one unit to the next
+//   kNarrow  rows are contiguous along k and start anywhere: the same in single loads (a row to a
+//            warp and 32 lanes along k took 109 us for what takes 74: addresses and stores)
+//   kAcross  contiguous along the tile's rows: the lanes in neighbouring rows
+enum Walk { kWide, kNarrow, kAcross };
+
+template <int W>
+__device__ __forceinline__ int row_of(int tid, int i) {  // of unit i
+  return W == kAcross ? tid & 127 : (tid >> 3) + 32 * i;
+}
+
+// at: row_of(tid, 0) at k = 0; step: to the next unit's row; ld: kAcross: from one k to the next;
+// ok: bit i: row_of(tid, i) exists; rows: of the operand's tile.
+template <int W>
+__device__ __forceinline__ void load_block(float (&v)[16], const float* at, int64_t step, uint32_t ok,
+                                           int64_t ld, int k0, int K, int rows, int tid) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (W != kAcross && 32 * i >= rows) break;
+    const int k = k0 + (W == kAcross ? (tid >> 7) + 2 * i : tid & 7) * 4;
+    const float* from = W == kAcross ? at + k * ld : at + i * step + k;
+    const bool mine = (ok >> i & 1u) != 0;
+    if constexpr (W == kWide) {
+      const float4 q = mine && k < K ? __ldg(reinterpret_cast<const float4*>(from))  // K % 4 == 0
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
+    } else if (k0 + kBK <= K) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * i + j] = mine ? __ldg(from + (W == kAcross ? j * ld : j)) : 0.0f;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[4 * i + j] = mine && k + j < K ? __ldg(from + (W == kAcross ? j * ld : j)) : 0.0f;
+    }
+  }
+}
+
+// hi: x cut to 11 bits (tf32); lo: the exact rest, rounded to 11. An infinite x gives an infinite hi
+// and a NaN lo, and so NaN sums.
+__device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = (__float_as_uint(x - __uint_as_float(hi)) + 0x1000u) & 0xffffe000u;
+}
+
+template <int W>
+__device__ __forceinline__ void put_block(const float (&v)[16], uint8_t* part, int rows, int tid) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (W != kAcross && 32 * i >= rows) break;
+    const int row = row_of<W>(tid, i), place = W == kAcross ? (tid >> 7) + 2 * i : tid & 7;
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split(v[4 * i + j], hi[j], lo[j]);
+    uint8_t* at = part + row * 128 + ((place ^ (row & 7)) << 4);
+    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(at + kPartBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+}
+
+__device__ __forceinline__ void tc_mma_tf32(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::tf32 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// What becomes of `n` sums of this lane's feature, of tile columns c.. on.
+template <int OP>
+__device__ __forceinline__ void finish(const Args& p, const Tile& w, const float (&s)[64], int c0, int quarter,
+                                       int lane) {
+  if constexpr (OP == kUp) {
+    // zg and zu of a feature lie half a warp apart: the lower lanes take columns 0..31, the upper
+    // ones 32..63
+    const int hi = lane >> 4, f = w.f0 + quarter * 16 + (lane & 15);
+    const bool f_ok = f < w.n_out;
+    const int64_t bi = (int64_t)w.e * w.n_out + f;
+    const float bg = p.bias0 != nullptr && f_ok ? p.bias0[bi] : 0.0f;
+    const float bu = p.bias1 != nullptr && f_ok ? p.bias1[bi] : 0.0f;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      const float own = hi ? s[32 + c] : s[c];
+      const float got = __shfl_xor_sync(0xffffffffu, hi ? s[c] : s[32 + c], 16);
+      const int col = c0 + hi * 32 + c;
+      if (f_ok && col < w.n_valid) {
+        const float zg = (hi ? got : own) + bg, zu = (hi ? own : got) + bu;
+        float a, da;
+        gate_act(zg, p.act, a, da);
+        const int64_t o = (int64_t)(w.row0 + col) * w.n_out + f;
+        p.out0[o] = a * zu;
+        if (p.out1 != nullptr) {
+          p.out1[o] = a;
+          p.out2[o] = zu * da;
+        }
+      }
+    }
+  } else {
+    const int f = w.f0 + quarter * 32 + lane;
+    if (f >= w.n_out) return;
+    const float b = OP == kDown && p.bias0 != nullptr ? p.bias0[(int64_t)w.e * w.n_out + f] : 0.0f;
+    float* out = OP == kWeight ? (w.which == 0 ? p.out0 : (w.which == 1 ? p.out1 : p.out2)) : p.out0;
+    // kWeight: a gradient row of this expert
+    const int64_t first = OP == kWeight ? (int64_t)w.e * (w.which == 0 ? p.d : p.f) : 0;
+#pragma unroll
+    for (int c = 0; c < 64; ++c) {
+      if (c0 + c >= w.n_valid) break;
+      const int64_t o = (first + w.row0 + c0 + c) * w.n_out + f;
+      if constexpr (OP == kHidden) {
+        const float a = p.in0[o], q = p.in1[o];
+        p.out0[o] = s[c] * q;  // dg
+        p.out1[o] = s[c] * a;  // du
+      } else {
+        out[o] = s[c] + b;
+      }
+    }
+  }
+}
+
+template <int OP, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 1) gated_tf32_kernel(const Args p) {
+  constexpr int kAlongK = WIDE ? kWide : kNarrow;
+  constexpr int kWalkA = OP == kUp || OP == kDown ? kAlongK : kAcross;
+  constexpr int kWalkB = OP == kWeight ? kAcross : kAlongK;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t base_addr = (raw_addr + 1023u) & ~1023u;
+  uint8_t* base = smem_raw + (base_addr - raw_addr);
+  uint8_t* aux = base + kStages * kStageBytes;
+  const uint32_t bars = smem_u32(aux);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(aux + kBarBytes);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(aux + kBarBytes + 4);
+  int* prefix = reinterpret_cast<int*>(aux + kBarBytes + 16);
+  int* seg = prefix + (MOE_MAX_EXPERTS + 1);
+  constexpr int S = kStages;
+  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
+  auto tfull_bar = [&](int a) { return bars + 8u * (2 * S + a); };
+  auto tempty_bar = [&](int a) { return bars + 8u * (2 * S + 2 + a); };
+  const uint32_t drain_bar = bars + 8u * (2 * S + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), kLoadWarps);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), kEpiWarps);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  pdl_wait();
+  if (warp == kLoadWarps) {
+    tmem_alloc(smem_u32(tmem_holder), kTmemCols);
+    tmem_relinquish();
+  }
+  if (OP != kWeight && warp == 0) {
+    constexpr int feat = OP == kUp ? kBM / 2 : kBM;
+    build_tile_list(p, (p.n_out + feat - 1) / feat, prefix, seg, lane);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const int total = tile_count<OP>(p, prefix);
+
+  if (warp < kLoadWarps) {
+    // ---------------------------------------------------------- loads and splits
+    const int tid = threadIdx.x;
+    const float *a_at = nullptr, *b_at = nullptr;  // this thread's first rows, for k = 0
+    uint32_t a_ok = 0, b_ok = 0;
+    int64_t a_ld = 0, b_ld = 0;
+    Tile w{};
+    int t = blockIdx.x, kb = 0, n_kb = 0, blocks1 = 0;
+    // makes (t, kb) the next K block there is; false if there is none
+    auto settle = [&]() {
+      while (t < total && kb >= n_kb) {
+        if (n_kb > 0) t += gridDim.x;
+        kb = n_kb = 0;
+        if (t >= total) return false;
+        w = tile_at<OP>(p, t, prefix, seg);
+        n_kb = k_blocks<OP>(w);
+        blocks1 = (w.K + kBK - 1) / kBK;
+        if (n_kb == 0) {
+          t += gridDim.x;
+          continue;
+        }
+        a_ok = b_ok = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // rows of the A tile: features in order, for kUp 16 of the gate's and 16 of the up
+          // projection's by turns
+          const int row = row_of<kWalkA>(tid, i);
+          if ((OP == kUp ? w.f0 + (row >> 5) * 16 + (row & 15) : w.f0 + row) < w.n_out)
+            a_ok |= 1u << i;
+          if (row_of<kWalkB>(tid, i) < w.n_valid) b_ok |= 1u << i;
+        }
+        const int row = row_of<kWalkA>(tid, 0), col = row_of<kWalkB>(tid, 0);
+        if constexpr (OP == kUp) {
+          a_at = (row & 16 ? p.a1 : p.a0) + ((int64_t)w.e * p.n_out + w.f0 + (row & 15)) * p.K;
+        } else if constexpr (OP == kDown) {
+          a_at = p.a0 + ((int64_t)w.e * p.n_out + w.f0 + row) * p.K;
+        } else if constexpr (OP == kWeight) {
+          a_at = (w.which == 0 ? p.a0 : p.a1) + (int64_t)w.seg * w.n_out + w.f0 + row;
+          a_ld = w.n_out;
+        } else {
+          a_at = p.a0 + (int64_t)w.e * p.K * p.n_out + w.f0 + row;
+          a_ld = p.n_out;
+        }
+        if constexpr (OP == kWeight) {
+          b_ld = w.which == 0 ? p.d : p.f;
+          b_at = (w.which == 0 ? p.b0 : (w.which == 1 ? p.b1 : p.b2)) + w.seg * b_ld + w.row0 + col;
+        } else {
+          b_at = p.b0 + ((int64_t)w.row0 + col) * p.K;
+        }
+      }
+      return t < total;
+    };
+    auto load = [&](float (&a)[16], float (&b)[16]) {
+      // kInput's second product: the same places of the other operands
+      const bool second = OP == kInput && kb >= blocks1;
+      const int k0 = (kb - (second ? blocks1 : 0)) * kBK;
+      load_block<kWalkA>(a, second ? p.a1 + (a_at - p.a0) : a_at, (int64_t)(OP == kUp ? 16 : 32) * p.K, a_ok,
+                         a_ld, k0, w.K, kBM, tid);
+      load_block<kWalkB>(b, second ? p.b1 + (b_at - p.b0) : b_at, (int64_t)32 * p.K, b_ok, b_ld, k0, w.K, p.bn,
+                         tid);
+      ++kb;
+    };
+    float av[16] = {}, bv[16] = {}, an[16] = {}, bn[16] = {};
+    int stage = 0;
+    uint32_t phase = 0;
+    bool have = settle();
+    if (have) load(av, bv);
+    while (have) {
+      const bool more = settle();
+      if (more) load(an, bn);
+      if (!mbar_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, p.status)) break;
+      uint8_t* to = base + stage * kStageBytes;
+      put_block<kWalkA>(av, to, kBM, tid);
+      put_block<kWalkB>(bv, to + 2 * kPartBytes, p.bn, tid);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full_bar(stage));
+      if (++stage == S) {
+        stage = 0;
+        phase ^= 1u;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        av[i] = an[i];
+        bv[i] = bn[i];
+      }
+      have = more;
+    }
+  } else if (warp == kLoadWarps) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const Tile w = tile_at<OP>(p, t, prefix, seg);
+        const int n_kb = k_blocks<OP>(w);
+        // D fp32, A and B tf32, K-major, N = the tile's columns in groups of 16
+        const uint32_t idesc = (1u << 4) | (2u << 7) | (2u << 10) |
+                               ((uint32_t)(((w.n_valid + 15) & ~15) >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
+        for (int kb = 0; kb < n_kb; ++kb) {
+          if (kb % kChunk == 0) {
+            if (!(ok = mbar_wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.status))) break;
+            tc_fence_after();
+          }
+          if (!(ok = mbar_wait_bounded(full_bar(stage), phase, abort_flag, p.status))) break;
+          tc_fence_after();
+          const uint32_t sa = base_addr + stage * kStageBytes;
+          const uint64_t a_hi = smem_desc_sw128(sa), a_lo = smem_desc_sw128(sa + kPartBytes);
+          const uint64_t b_hi = smem_desc_sw128(sa + 2 * kPartBytes);
+          const uint64_t b_lo = smem_desc_sw128(sa + 3 * kPartBytes);
+          const uint32_t d = tmem_base + (uint32_t)(acc * kAccCols);
+          const uint32_t first = kb % kChunk == 0 ? 0u : 1u;
+#pragma unroll
+          for (int kk = 0; kk < kBK / 8; ++kk) {
+            tc_mma_tf32(d, a_hi + 2 * kk, b_hi + 2 * kk, idesc, kk != 0 ? 1u : first);
+            tc_mma_tf32(d + kBN, a_lo + 2 * kk, b_hi + 2 * kk, idesc, kk != 0 ? 1u : first);
+            tc_mma_tf32(d + kBN, a_hi + 2 * kk, b_lo + 2 * kk, idesc, 1u);
+          }
+          tc_commit(empty_bar(stage));
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (kb % kChunk == kChunk - 1 || kb == n_kb - 1) {
+            tc_commit(tfull_bar(acc));
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+          }
+        }
+      }
+      // drain every MMA this thread issued before TMEM is released
+      tc_commit(drain_bar);
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(drain_bar, 0))
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+          set_device_error(p.status, MOE_DEVERR_TIMEOUT);
+          break;
+        }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- epilogue: half of the columns each
+    const int quarter = warp & 3, c0 = (warp - kLoadWarps - 1) / 4 * 64;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const Tile w = tile_at<OP>(p, t, prefix, seg);
+      const int chunks = (k_blocks<OP>(w) + kChunk - 1) / kChunk;
+      float s[64];
+#pragma unroll
+      for (int c = 0; c < 64; ++c) s[c] = 0.0f;
+      for (int k = 0; k < chunks; ++k) {
+        if (!(ok = mbar_wait_warp(tfull_bar(acc), acc_phase, abort_flag, p.status))) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kAccCols + c0);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (c0 + g * 16 < w.n_valid) {
+            uint32_t r[16];
+#pragma unroll
+            for (int part = 1; part >= 0; --part) {
+              tmem_ld_32x32b_x16(taddr + (uint32_t)(part * kBN + g * 16), r);
+              tmem_ld_wait16(r);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) s[g * 16 + c] += __uint_as_float(r[c]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty_bar(acc));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (ok && c0 < w.n_valid) finish<OP>(p, w, s, c0, quarter, lane);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  pdl_trigger();
+  if (warp == kLoadWarps) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+template <int OP, bool WIDE>
+cudaError_t launch_walk(const Args& p, unsigned grid, cudaStream_t stream) {
+  static int attr_done[64] = {0};  // per instantiation and device
+  const cudaError_t e = ensure_dynamic_smem(gated_tf32_kernel<OP, WIDE>, kSmemBytes, attr_done);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(gated_tf32_kernel<OP, WIDE>, dim3(grid), dim3(kThreads), kSmemBytes, stream, p);
+}
+
+template <int OP>
+cudaError_t launch(Args& p, int64_t capacity_hint, cudaStream_t stream) {
+  if (p.rows_max == 0) return cudaSuccess;
+  // tiles as far as the host knows
+  auto tiles = [&](int bn) -> int64_t {
+    auto over = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
+    if (OP == kWeight) return p.E * (over(p.f, kBM) * over(p.d, bn) + 2 * over(p.d, kBM) * over(p.f, bn));
+    const int64_t rows = std::max<int64_t>(1, std::min(capacity_hint, p.rows_max));
+    return std::min<int64_t>(p.E, p.rows_max) * over(rows, bn) * over(p.n_out, OP == kUp ? kBM / 2 : kBM);
+  };
+  p.bn = tiles(kBN) < num_sms() ? 64 : kBN;
+  // K % 4 == 0: rows that are contiguous along k start on 16 bytes
+  const unsigned grid = (unsigned)std::min<int64_t>(tiles(p.bn), num_sms());
+  return OP != kWeight && p.K % 4 == 0 ? launch_walk<OP, OP != kWeight>(p, grid, stream)
+                                       : launch_walk<OP, false>(p, grid, stream);
+}
+
+Args args_of(const GatedFfn& g, int* status) {
+  Args p{};
+  p.offsets = g.offsets; p.E = g.E; p.d = g.d; p.f = g.f; p.act = g.act; p.rows_max = g.rows_max;
+  p.status = status;
+  return p;
+}
+
+}  // namespace
+
+cudaError_t enqueue_gated_up_f32(const GatedFfn& g, float* h, float* saved_a, float* saved_q,
+                                 int* status, cudaStream_t stream) {
+  Args p = args_of(g, status);
+  p.n_out = g.f; p.K = g.d;
+  p.a0 = (const float*)g.w_gate; p.a1 = (const float*)g.w_up; p.b0 = (const float*)g.x;
+  p.bias0 = (const float*)g.b_gate; p.bias1 = (const float*)g.b_up;
+  p.out0 = h; p.out1 = saved_a; p.out2 = saved_q;
+  return launch<kUp>(p, g.capacity_hint, stream);
+}
+
+cudaError_t enqueue_gated_down_f32(const GatedFfn& g, const float* h, float* y, int* status,
+                                   cudaStream_t stream) {
+  Args p = args_of(g, status);
+  p.n_out = g.d; p.K = g.f;
+  p.a0 = (const float*)g.w_down; p.b0 = h; p.bias0 = (const float*)g.b_down; p.out0 = y;
+  return launch<kDown>(p, g.capacity_hint, stream);
+}
+
+cudaError_t enqueue_gated_hidden_grad_f32(const GatedFfn& g, const float* dy, const float* saved_a,
+                                          const float* saved_q, float* dg, float* du, int* status,
+                                          cudaStream_t stream) {
+  Args p = args_of(g, status);
+  p.n_out = g.f; p.K = g.d;
+  p.a0 = (const float*)g.w_down; p.b0 = dy; p.in0 = saved_a; p.in1 = saved_q;
+  p.out0 = dg; p.out1 = du;
+  return launch<kHidden>(p, g.capacity_hint, stream);
+}
+
+cudaError_t enqueue_gated_input_grad_f32(const GatedFfn& g, const float* dg, const float* du,
+                                         float* dx, int* status, cudaStream_t stream) {
+  Args p = args_of(g, status);
+  p.n_out = g.d; p.K = g.f;
+  p.a0 = (const float*)g.w_gate; p.a1 = (const float*)g.w_up; p.b0 = dg; p.b1 = du;
+  p.out0 = dx;
+  return launch<kInput>(p, g.capacity_hint, stream);
+}
+
+cudaError_t enqueue_gated_weight_grad_f32(const GatedFfn& g, const float* dy, const float* h,
+                                          const float* dg, const float* du, float* dw_down,
+                                          float* dw_gate, float* dw_up, int* status,
+                                          cudaStream_t stream) {
+  Args p = args_of(g, status);
+  p.a0 = h; p.a1 = (const float*)g.x; p.b0 = dy; p.b1 = dg; p.b2 = du;
+  p.out0 = dw_down; p.out1 = dw_gate; p.out2 = dw_up;
+  return launch<kWeight>(p, g.capacity_hint, stream);
+}
+
+}  // namespace moe

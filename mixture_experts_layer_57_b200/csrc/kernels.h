@@ -357,7 +357,7 @@ cudaError_t enqueue_simt_gemm(const SimtGemm& p, int64_t m_extent, cudaStream_t 
 
 // ---------------------------------------------------------------- gated expert FFN
 // h = act(Wg[e] x + bg[e]) * (Wu[e] x + bu[e]), y = Wd[e] h + bd[e] on expert-major rows, and its
-// backward pass (f32: fp32 FMA kernels; bf16: tcgen05 kernels). saved_a = act(zg) and saved_q =
+// backward pass, on tcgen05 (f32: with every factor split in two tf32 parts). saved_a = act(zg) and saved_q =
 // zu act'(zg) are what the backward pass needs of the pre-activations (NULL: not kept).
 struct GatedFfn {
   const int32_t* offsets;
