@@ -417,14 +417,15 @@ moe_status moe_layer_backward(const moe_layer_args* args, const void* d_out, flo
  * saved: NULL, or [2, rows_max, d_ff] in dtype for the backward pass, which alone reads it: plane 0
  * receives act(zg), plane 1 zu act'(zg) (bf16 layers: eight neighbours in 16 bits each with one
  * exponent between them, 11 bits where bf16 would keep 8).
- * Rows outside every segment are neither read nor written. Offsets that are not non-decreasing
- * within [0, rows_max] set MOE_DEVERR_BAD_OFFSETS. capacity_hint: an upper bound on the rows of
+ * Rows outside every segment are not written and their values do not matter (NaN included). No
+ * output may overlap another tensor of the call; inputs may (w_up may be w_gate). Offsets that are
+ * not non-decreasing within [0, rows_max] set MOE_DEVERR_BAD_OFFSETS. capacity_hint: an upper bound on the rows of
  * any one expert (normally C); it selects tile sizes and how sums are split, so it may change
  * results in their rounding, and is otherwise free to be wrong.
  * Limits: those of moe_expert_ffn (bf16: d_model and d_ff multiples of 8). Both types run on tcgen05
  * tensor cores and accumulate in fp32. fp32 factors are split in two tf32 parts each, which keeps
- * sums as exact as fp32 FMAs' (products within 2^-20, 2^-23 on average); there an infinite factor
- * makes its sums NaN. */
+ * sums as exact as fp32 FMAs' (products within 2^-21); there an infinite factor may make its sums
+ * NaN. fp32 calls of up to 8 rows without saved run on fp32 FMA. */
 typedef enum { MOE_GATE_SILU = 0, MOE_GATE_GELU = 1 } moe_gate_act;
 typedef struct {
   const void* x_packed;
@@ -448,10 +449,10 @@ moe_status moe_gated_ffn(const moe_gated_ffn_args* args, void* h_packed, void* y
  *     dx = dg w_gate[e] + du w_up[e],
  *     dw_down[e] = dy^T h,  dw_gate[e] = dg^T x,  dw_up[e] = du^T x   (sums over e's rows),
  *     db_down, db_gate, db_up: the column sums of dy, dg, du.
- * Gradients are overwritten; experts without rows get zeros. dx_packed [rows_max, d_model] in
- * dx_dtype (rows outside every segment are not written); the weight and bias gradients in
- * grad_dtype, in the parameters' shapes; bias gradients may be NULL (not computed). fp32 layers
- * take MOE_F32 for both types. bf16 layers round dg and du to bf16 (the operands of the products
+ * Gradients are overwritten, and overlap no other tensor of the call; experts without rows get
+ * zeros. dx_packed [rows_max, d_model] in dx_dtype (rows outside every segment are not written);
+ * the weight and bias gradients in grad_dtype, in the parameters' shapes; bias gradients may be
+ * NULL (not computed). fp32 layers take MOE_F32 for both types. bf16 layers round dg and du to bf16 (the operands of the products
  * that follow) and accumulate in fp32. */
 typedef struct {
   void* dx_packed;

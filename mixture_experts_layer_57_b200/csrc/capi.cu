@@ -1398,7 +1398,9 @@ moe_status moe_gated_ffn(const moe_gated_ffn_args* args, void* h_packed, void* y
   const GatedFfn g = gated_of(args);
   int* status = (int*)ws;
   cudaError_t e;
-  if (args->dtype == MOE_BF16) {
+  if (args->dtype == MOE_F32 && saved == nullptr && args->rows_max <= kGatedGemvRows) {
+    e = enqueue_gated_gemv_f32(g, (float*)h_packed, (float*)y_packed, status, stream);
+  } else if (args->dtype == MOE_BF16) {
     e = enqueue_gated_up_bf16(g, h_packed, saved, saved_q, status, stream);
     if (e == cudaSuccess)
       e = enqueue_gated_down_bf16(g, h_packed, y_packed, args->out_dtype == MOE_BF16, status, stream);

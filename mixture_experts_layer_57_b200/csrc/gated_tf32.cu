@@ -6,14 +6,14 @@
 //     input   dx[r, :] = Wg[e]^T dg[r, :] + Wu[e]^T du[r, :]
 //     weight  dWd[e] = dy^T h,  dWg[e] = dg^T x,  dWu[e] = du^T x   (sums over the rows of e)
 //
-// Sums as exact as fp32 arithmetic's. Every factor is split in two tf32 numbers, hi = x cut to 11
-// bits and lo = x - hi rounded to 11, together within 2^-22 of x, and a product is hi hi + hi lo +
-// lo hi: lo lo, which is left out, is 2^-20 of it at most and 2^-23 on average. The tensor cores cut
-// each sum towards zero instead of rounding it (measured: 31 additions of 1.94 2^-24 to 1 leave 1),
-// which over a long sum would cost several bits. So hi hi and the other two, 2^-10 of it, have
-// accumulators of their own, 64 of K are summed in TMEM at a time, and the epilogue warps add those
-// sums in registers, rounded to nearest. Measured against 64 bits, relative to the whole output
-// (1000 rows, d 501, f 1334): 7e-7, where fp32 FMAs in index order gave 9e-7.
+// Sums as exact as fp32 arithmetic's. Every factor is split in two tf32 numbers, hi = x rounded to
+// 11 bits and lo = x - hi rounded to 11, together within 2^-23 of x, and a product is hi hi + hi lo +
+// lo hi: lo lo, which is left out, is 2^-22 of it at most, of either sign. The tensor cores cut each
+// sum towards zero instead of rounding it (measured: 31 additions of 1.94 2^-24 to 1 leave 1), which
+// over a long sum would cost several bits. So hi hi and the other two, 2^-11 of it, have accumulators
+// of their own, 64 of K are summed in TMEM at a time, and the epilogue warps add those sums in
+// registers, rounded to nearest. Measured against 64 bits, relative to the whole output (1000 rows,
+// d 501, f 1334): @@, where fp32 FMAs in index order gave 9e-7.
 //
 // Operands have any width, so rows start on any multiple of 4 bytes, which no TMA copy can do: eight
 // warps load them (the next block's while they split this one's), split, and write both parts
@@ -197,11 +197,19 @@ __device__ __forceinline__ void load_block(float (&v)[16], const float* at, int6
   }
 }
 
-// hi: x cut to 11 bits (tf32); lo: the exact rest, rounded to 11. An infinite x gives an infinite hi
-// and a NaN lo, and so NaN sums.
-__device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
-  hi = __float_as_uint(x) & 0xffffe000u;
-  lo = (__float_as_uint(x - __uint_as_float(hi)) + 0x1000u) & 0xffffe000u;
+// hi: x rounded to 11 bits (tf32), lo: the exact rest, rounded to 11. Where one of the four is 2^127
+// or more, infinite or NaN, hi is cut instead: it neither overflows nor loses a NaN. An infinite x may
+// make NaN of its sums (with a zero lo of the other factor).
+__device__ __forceinline__ void split4(const float* x, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  float m = fabsf(x[0]);
+#pragma unroll
+  for (int j = 1; j < 4; ++j) asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(fabsf(x[j])));
+  const uint32_t half = m < 1.7014118346e38f ? 0x1000u : 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    hi[j] = (__float_as_uint(x[j]) + half) & 0xffffe000u;
+    lo[j] = (__float_as_uint(x[j] - __uint_as_float(hi[j])) + 0x1000u) & 0xffffe000u;
+  }
 }
 
 template <int W>
@@ -211,8 +219,7 @@ __device__ __forceinline__ void put_block(const float (&v)[16], uint8_t* part, i
     if (W != kAcross && 32 * i >= rows) break;
     const int row = row_of<W>(tid, i), place = W == kAcross ? (tid >> 7) + 2 * i : tid & 7;
     uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) split(v[4 * i + j], hi[j], lo[j]);
+    split4(v + 4 * i, hi, lo);
     uint8_t* at = part + row * 128 + ((place ^ (row & 7)) << 4);
     *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(at + kPartBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);

@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(128) gated_bias_grad_kernel(const BiasParams p
     float acc[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) acc[v] = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t r = r0; r < r1; ++r) {
       if constexpr (BF16) {
         const uint4 q = *reinterpret_cast<const uint4*>(
@@ -498,10 +498,13 @@ __global__ void __launch_bounds__(256) gated_bias_join_kernel(const BiasParams p
   pdl_trigger();
 }
 
-// Row splits: enough blocks to fill the SMs a few times when there are few experts.
+// Row splits: a thread adds its rows one after another, so few experts' rows are cut into some 200
+// parts of 32 rows or more (17 experts, 1637 rows, 6520 columns:
+// 16 us and 4 to join, 26 and 4 with parts of 256).
 int bias_splits(int E, int64_t rows_max) {
-  const int64_t per = (rows_max + 255) / 256;  // 256 rows to a split at least
-  int64_t s = (64 + E - 1) / E;
+  const int64_t per = (rows_max + 31) / 32;
+  int64_t s = (200 + E - 1) / E;
+  if (s > 64) s = 64;
   if (s > per) s = per;
   return (int)(s < 1 ? 1 : s);
 }

@@ -392,6 +392,10 @@ cudaError_t enqueue_gated_weight_grad_bf16(const GatedFfn& g, const void* dy, co
                                            const void* dg, const void* du, void* dw_down,
                                            void* dw_gate, void* dw_up, bool grad_bf16, int* status,
                                            cudaStream_t stream);
+// The forward pass of up to kGatedGemvRows fp32 rows, both launches, without the saved tensors.
+constexpr int kGatedGemvRows = 8;
+cudaError_t enqueue_gated_gemv_f32(const GatedFfn& g, float* h, float* y, int* status,
+                                   cudaStream_t stream);
 // Bias gradients: column sums of up to three matrices over each segment's rows, in one launch
 // (and a second one that adds the row splits). Any out may be NULL.
 struct GatedBiasGrad {

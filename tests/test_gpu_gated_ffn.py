@@ -356,3 +356,92 @@ def test_bf16_infinity_in_one_feature(cuda_ok):
     far = torch.arange(128, device="cuda") >= 8
     assert torch.equal(got["dw_up"][0, far], clean["dw_up"][0, far])
     assert bool(torch.isfinite(got["dw_up"][0, near]).all())
+
+
+@pytest.mark.parametrize("counts", [[1], [2], [3], [4], [5], [8], [1, 0, 2, 0, 1], [0, 0, 3, 4, 0, 1], [0, 1, 0]],
+                         ids=str)
+@pytest.mark.parametrize("dtype,d,f", [(torch.bfloat16, 264, 520), (torch.bfloat16, 8, 24),
+                                       (torch.float32, 257, 77), (torch.float32, 33, 131)], ids=str)
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_few_rows_forward(cuda_ok, counts, dtype, d, f, act):
+    # without the saved tensors, as decoding runs it; rows before and behind the segments stay
+    for first, slack in ((0, 0), (2, 1)):
+        c = make(len(counts), counts, d, f, dtype, seed=d + len(counts), first=first, slack=slack)
+        for out_dtype in {dtype, torch.float32}:
+            y = torch.full(c["x"].shape, SENTINEL, dtype=out_dtype, device="cuda")
+            r = moe.moe_gated_ffn(args_of(c, act, out_dtype), y_packed=y)
+            assert moe.moe_get_device_error(r["ws"]) == 0
+            a = first
+            for e, n in enumerate(counts):
+                if n:
+                    params = {k: None if c[k] is None else c[k][e] for k in NAMES}
+                    gated_ref.check(f"expert {e}: y", y[a:a + n],
+                                    *gated_ref.segment(c["x"][a:a + n], params, act)["y"])
+                a += n
+            assert bool((y[:first] == SENTINEL).all()) and bool((y[a:] == SENTINEL).all())
+
+
+def test_few_rows_bad_offsets(cuda_ok):
+    for dtype in (torch.float32, torch.bfloat16):
+        c = make(2, [2, 1], 64, 128, dtype, seed=19, slack=0)
+        c["off"] = torch.tensor([0, 2, 1], dtype=torch.int32, device="cuda")
+        y = torch.full(c["x"].shape, SENTINEL, dtype=dtype, device="cuda")
+        r = moe.moe_gated_ffn(args_of(c), y_packed=y)
+        assert moe.moe_get_device_error(r["ws"]) == 3
+        assert bool((y == SENTINEL).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_one_tensor_for_both_projections(cuda_ok, dtype):
+    c = make(2, [33, 150], 128, 272, dtype, seed=20)
+    c["w_up"] = c["w_gate"]
+    got, kept = run(c, "silu")
+    compare(c, got, "silu", kept)
+
+
+def test_up_weights_before_gate_weights(cuda_ok):
+    # the projections in one allocation, in either order, and with a width off the 16-row groups
+    for d, f in ((128, 272), (128, 264)):
+        c = make(2, [33, 150], d, f, torch.bfloat16, seed=21)
+        both = torch.empty(2, 2, f, d, dtype=torch.bfloat16, device="cuda")
+        for order in (("w_gate", "w_up"), ("w_up", "w_gate")):
+            e = dict(c)
+            for i, n in enumerate(order):
+                both[i].copy_(c[n])
+                e[n] = both[i]
+            got, kept = run(e, "gelu")
+            compare(e, got, "gelu", kept)
+
+
+def test_two_streams_at_once(cuda_ok):
+    cases = [make(6, [40, 0, 130, 7, 64, 300], 264, 520, torch.bfloat16, seed=22),
+             make(3, [100, 30, 1], 257, 131, torch.float32, seed=23)]
+    want = [run(c, "silu")[0] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    out = []
+    for _ in range(5):
+        for c, s in zip(cases, streams):
+            args = args_of(c)
+            r = moe.moe_gated_ffn(args, train=True, stream=s)
+            g = moe.moe_gated_ffn_backward(args, c["dy"], r["h_packed"], r["saved"],
+                                           grad_dtype=c["x"].dtype, stream=s)
+            out.append((r["y_packed"], g))
+    torch.cuda.synchronize()
+    for i, (y, g) in enumerate(out):
+        w, n = want[i % 2], sum(cases[i % 2]["counts"])
+        assert torch.equal(y[:n], w["y"][:n]) and torch.equal(g["dx_packed"][:n], w["dx_packed"][:n])
+        for k in NAMES:
+            assert torch.equal(g["d" + k], w["d" + k]), k
+
+
+def test_stream_of_no_such_device_is_refused(cuda_ok):
+    c = make(1, [4], 64, 72, torch.bfloat16, seed=24)
+
+    class Elsewhere:
+        device, cuda_stream = torch.device("cuda", 7), 0
+
+    with pytest.raises(ValueError):
+        moe.moe_gated_ffn(args_of(c), stream=Elsewhere())
+    with pytest.raises(ValueError):
+        moe.moe_grad_norm([c["x"]], stream=Elsewhere())
