@@ -13,15 +13,15 @@
 // over a long sum would cost several bits. So hi hi and the other two, 2^-11 of it, have accumulators
 // of their own, 64 of K are summed in TMEM at a time, and the epilogue warps add those sums in
 // registers, rounded to nearest. Measured against 64 bits, relative to the whole output (1000 rows,
-// d 501, f 1334): @@, where fp32 FMAs in index order gave 9e-7.
+// d 501, f 1334): 5e-7, where fp32 FMAs in index order gave 9e-7.
 //
 // Operands have any width, so rows start on any multiple of 4 bytes, which no TMA copy can do: eight
 // warps load them (the next block's while they split this one's), split, and write both parts
 // K-major in the swizzled layout of the MMA. The lanes of the accumulator are the output's
-// contiguous index, so stores go out as whole lines. Tiles are 128 x 128, or 128 x 64 where the
-// former are fewer than the SMs. What bounds it: the loads and splits, some 3000 cycles for 32 of K
-// (three tf32 MMA passes: 768). 4 experts, 1000 rows, d 501, f 1334: up 68 us, down 63 (tiles of
-// fp32 FMAs: 123 and 115).
+// contiguous index, so stores go out as whole lines. Tiles are of 128 features and 128 or 64 rows, or
+// 64 rows with K over clusters of four CTAs that exchange their sums (launch_walk chooses). What
+// bounds it: the loads and splits, some 2000 cycles for 32 of K and 128 rows (three tf32 MMA passes:
+// 768). 4 experts, 1000 rows, d 501, f 1334: up 67 us, down 60 (tiles of fp32 FMAs: 123 and 115).
 #include <algorithm>
 
 #include "common.cuh"
@@ -33,25 +33,37 @@ namespace {
 
 enum Op { kUp = 0, kDown = 1, kHidden = 2, kInput = 3, kWeight = 4 };
 
-constexpr int kBM = 128, kBN = 128;
+constexpr int kBM = 128;
 constexpr int kBK = 32;                  // fp32 of K per stage: one 128-byte swizzle row
 constexpr int kChunk = 2;                // K blocks per sum in TMEM
-constexpr int kStages = 3;
-constexpr int kPartBytes = kBM * kBK * 4;        // one part (hi or lo) of one operand
-constexpr int kStageBytes = 4 * kPartBytes;      // A hi, A lo, B hi, B lo
 constexpr int kLoadWarps = 8, kEpiWarps = 8;
 // One warp of MMAs: 17 warps, for which the register file leaves 96 a thread.
 constexpr int kThreads = 32 * (kLoadWarps + 1 + kEpiWarps);
-constexpr int kAccCols = 2 * kBN;        // hi hi, and the small products
-constexpr int kTmemCols = 2 * kAccCols;  // two of both
+constexpr int kAPart = kBM * kBK * 4;    // one part (hi or lo) of A
 constexpr int kBarBytes = 8 * 16;
-constexpr int kSmemBytes =
-    1024 + kStages * kStageBytes + kBarBytes + 16 + 2 * 4 * (MOE_MAX_EXPERTS + 1);
-static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+
+// BN: token columns of a tile. SPLIT: CTAs of a cluster that share a tile, each with its part of the
+// K blocks; each then finishes every SPLIT-th part of every epilogue warp's columns, for which all
+// write their sums into its shared memory.
+template <int BN, int SPLIT>
+struct Cfg {
+  static constexpr int kBPart = BN * kBK * 4;
+  static constexpr int kStageBytes = 2 * kAPart + 2 * kBPart;  // A hi, A lo, B hi, B lo
+  static constexpr int kCols = BN / 2;                         // columns of an epilogue warp
+  static constexpr int kOwn = kCols / SPLIT;                   // that this CTA finishes
+  static constexpr int kExchange = SPLIT > 1 ? kEpiWarps * kCols * 32 * 4 : 0;
+  static constexpr int kStages = BN == 128 || SPLIT > 1 ? 3 : 4;
+  static constexpr int kAccCols = 2 * BN;                      // hi hi, and the small products
+  static constexpr int kTmemCols = 2 * kAccCols;               // two of both
+  static constexpr int kSmemBytes =
+      1024 + kStages * kStageBytes + kExchange + kBarBytes + 16 + 2 * 4 * (MOE_MAX_EXPERTS + 1);
+  static_assert(kSmemBytes <= 227 * 1024 && kOwn % 2 == 0, "shared memory budget, halves of kUp");
+  static_assert(2 * kStages + 7 <= kBarBytes / 8, "barrier area too small");
+};
 
 struct Args {
   const int32_t* offsets;
-  int E, act, bn;
+  int E, act;
   int64_t rows_max;
   int n_out;                 // output features (kWeight: unused)
   int K;                     // of each product (kWeight: unused, the segment's rows)
@@ -70,31 +82,31 @@ struct Tile {
   int e, f0, row0, n_valid, which, n_out, K, seg;
 };
 
-template <int OP>
+template <int OP, int BN>
 __device__ __forceinline__ int tile_count(const Args& p, const int* prefix) {
   if constexpr (OP != kWeight) return prefix[p.E];
-  const int t0 = ((p.f + kBM - 1) / kBM) * ((p.d + p.bn - 1) / p.bn);
-  const int t1 = ((p.d + kBM - 1) / kBM) * ((p.f + p.bn - 1) / p.bn);
+  const int t0 = ((p.f + kBM - 1) / kBM) * ((p.d + BN - 1) / BN);
+  const int t1 = ((p.d + kBM - 1) / kBM) * ((p.f + BN - 1) / BN);
   return p.E * (t0 + 2 * t1);
 }
 
-template <int OP>
+template <int OP, int BN>
 __device__ __forceinline__ Tile tile_at(const Args& p, int t, const int* prefix, const int* seg) {
   Tile w;
   if constexpr (OP == kWeight) {
     // dWd [d, f], then dWg and dWu [f, d]: features are a gradient row's elements
-    const int t0 = ((p.f + kBM - 1) / kBM) * ((p.d + p.bn - 1) / p.bn);
-    const int t1 = ((p.d + kBM - 1) / kBM) * ((p.f + p.bn - 1) / p.bn);
+    const int t0 = ((p.f + kBM - 1) / kBM) * ((p.d + BN - 1) / BN);
+    const int t1 = ((p.d + kBM - 1) / kBM) * ((p.f + BN - 1) / BN);
     w.e = t / (t0 + 2 * t1);
     int u = t - w.e * (t0 + 2 * t1);
     w.which = u < t0 ? 0 : 1 + (u - t0) / t1;
     if (w.which != 0) u = (u - t0) % t1;
     w.n_out = w.which == 0 ? p.f : p.d;
     const int rows = w.which == 0 ? p.d : p.f;
-    const int nt = (rows + p.bn - 1) / p.bn;
+    const int nt = (rows + BN - 1) / BN;
     w.f0 = u / nt * kBM;
-    w.row0 = u % nt * p.bn;
-    w.n_valid = min(p.bn, rows - w.row0);
+    w.row0 = u % nt * BN;
+    w.n_valid = min(BN, rows - w.row0);
     int a = __ldg(p.offsets + w.e), b = __ldg(p.offsets + w.e + 1);
     if (a < 0 || b < a || (int64_t)b > p.rows_max) a = b = 0;  // flagged by the passes before
     w.seg = a;
@@ -106,12 +118,12 @@ __device__ __forceinline__ Tile tile_at(const Args& p, int t, const int* prefix,
       if (prefix[mid] <= t) lo = mid;
       else hi = mid;
     }
-    const int rows = seg[lo + 1] - seg[lo], ntt = (rows + p.bn - 1) / p.bn;
+    const int rows = seg[lo + 1] - seg[lo], ntt = (rows + BN - 1) / BN;
     const int local = t - prefix[lo], ft = local / ntt, jt = local - ft * ntt;
     w.e = lo;
     w.f0 = ft * (OP == kUp ? kBM / 2 : kBM);
-    w.row0 = seg[lo] + jt * p.bn;
-    w.n_valid = min(p.bn, rows - jt * p.bn);
+    w.row0 = seg[lo] + jt * BN;
+    w.n_valid = min(BN, rows - jt * BN);
     w.which = 0;
     w.n_out = p.n_out;
     w.K = p.K;
@@ -127,6 +139,7 @@ __device__ __forceinline__ int k_blocks(const Tile& w) {
 
 // One warp: seg[e] and the first tile of every expert; none if the offsets are not non-decreasing
 // within [0, rows_max], which is flagged.
+template <int BN>
 __device__ __forceinline__ void build_tile_list(const Args& p, int n_ftiles, int* prefix, int* seg,
                                                 int lane) {
   int run = 0;
@@ -138,7 +151,7 @@ __device__ __forceinline__ void build_tile_list(const Args& p, int n_ftiles, int
       const int a = p.offsets[e], b = p.offsets[e + 1];
       seg[e] = a;
       if (a < 0 || b < a || (int64_t)b > p.rows_max) bad = true;
-      else tiles = n_ftiles * ((b - a + p.bn - 1) / p.bn);
+      else tiles = n_ftiles * ((b - a + BN - 1) / BN);
     }
     int incl = tiles;
 #pragma unroll
@@ -166,20 +179,24 @@ __device__ __forceinline__ void build_tile_list(const Args& p, int n_ftiles, int
 //   kAcross  contiguous along the tile's rows: the lanes in neighbouring rows
 enum Walk { kWide, kNarrow, kAcross };
 
-template <int W>
-__device__ __forceinline__ int row_of(int tid, int i) {  // of unit i
-  return W == kAcross ? tid & 127 : (tid >> 3) + 32 * i;
+// Of a tile of R rows, R / 32 units a thread: row and 16-byte place of unit i.
+template <int W, int R>
+__device__ __forceinline__ int row_of(int tid, int i) {
+  return W == kAcross ? tid % R : (tid >> 3) + 32 * i;
+}
+template <int W, int R>
+__device__ __forceinline__ int place_of(int tid, int i) {
+  return W == kAcross ? tid / R + (256 / R) * i : tid & 7;
 }
 
 // at: row_of(tid, 0) at k = 0; step: to the next unit's row; ld: kAcross: from one k to the next;
-// ok: bit i: row_of(tid, i) exists; rows: of the operand's tile.
-template <int W>
-__device__ __forceinline__ void load_block(float (&v)[16], const float* at, int64_t step, uint32_t ok,
-                                           int64_t ld, int k0, int K, int rows, int tid) {
+// ok: bit i: row_of(tid, i) exists.
+template <int W, int R>
+__device__ __forceinline__ void load_block(float (&v)[R / 8], const float* at, int64_t step, uint32_t ok,
+                                           int64_t ld, int k0, int K, int tid) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (W != kAcross && 32 * i >= rows) break;
-    const int k = k0 + (W == kAcross ? (tid >> 7) + 2 * i : tid & 7) * 4;
+  for (int i = 0; i < R / 32; ++i) {
+    const int k = k0 + place_of<W, R>(tid, i) * 4;
     const float* from = W == kAcross ? at + k * ld : at + i * step + k;
     const bool mine = (ok >> i & 1u) != 0;
     if constexpr (W == kWide) {
@@ -212,17 +229,16 @@ __device__ __forceinline__ void split4(const float* x, uint32_t (&hi)[4], uint32
   }
 }
 
-template <int W>
-__device__ __forceinline__ void put_block(const float (&v)[16], uint8_t* part, int rows, int tid) {
+template <int W, int R>
+__device__ __forceinline__ void put_block(const float (&v)[R / 8], uint8_t* part, int tid) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (W != kAcross && 32 * i >= rows) break;
-    const int row = row_of<W>(tid, i), place = W == kAcross ? (tid >> 7) + 2 * i : tid & 7;
+  for (int i = 0; i < R / 32; ++i) {
+    const int row = row_of<W, R>(tid, i), place = place_of<W, R>(tid, i);
     uint32_t hi[4], lo[4];
     split4(v + 4 * i, hi, lo);
     uint8_t* at = part + row * 128 + ((place ^ (row & 7)) << 4);
     *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(at + kPartBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(at + R * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
 
@@ -236,23 +252,23 @@ __device__ __forceinline__ void tc_mma_tf32(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
-// What becomes of `n` sums of this lane's feature, of tile columns c.. on.
-template <int OP>
-__device__ __forceinline__ void finish(const Args& p, const Tile& w, const float (&s)[64], int c0, int quarter,
+// What becomes of N sums of this lane's feature, of tile columns c0.. on.
+template <int OP, int N>
+__device__ __forceinline__ void finish(const Args& p, const Tile& w, const float (&s)[N], int c0, int quarter,
                                        int lane) {
   if constexpr (OP == kUp) {
-    // zg and zu of a feature lie half a warp apart: the lower lanes take columns 0..31, the upper
-    // ones 32..63
+    // zg and zu of a feature lie half a warp apart: the lower lanes take the first half of the
+    // columns, the upper ones the second
     const int hi = lane >> 4, f = w.f0 + quarter * 16 + (lane & 15);
     const bool f_ok = f < w.n_out;
     const int64_t bi = (int64_t)w.e * w.n_out + f;
     const float bg = p.bias0 != nullptr && f_ok ? p.bias0[bi] : 0.0f;
     const float bu = p.bias1 != nullptr && f_ok ? p.bias1[bi] : 0.0f;
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      const float own = hi ? s[32 + c] : s[c];
-      const float got = __shfl_xor_sync(0xffffffffu, hi ? s[c] : s[32 + c], 16);
-      const int col = c0 + hi * 32 + c;
+    for (int c = 0; c < N / 2; ++c) {
+      const float own = hi ? s[N / 2 + c] : s[c];
+      const float got = __shfl_xor_sync(0xffffffffu, hi ? s[c] : s[N / 2 + c], 16);
+      const int col = c0 + hi * (N / 2) + c;
       if (f_ok && col < w.n_valid) {
         const float zg = (hi ? got : own) + bg, zu = (hi ? own : got) + bu;
         float a, da;
@@ -273,7 +289,7 @@ __device__ __forceinline__ void finish(const Args& p, const Tile& w, const float
     // kWeight: a gradient row of this expert
     const int64_t first = OP == kWeight ? (int64_t)w.e * (w.which == 0 ? p.d : p.f) : 0;
 #pragma unroll
-    for (int c = 0; c < 64; ++c) {
+    for (int c = 0; c < N; ++c) {
       if (c0 + c >= w.n_valid) break;
       const int64_t o = (first + w.row0 + c0 + c) * w.n_out + f;
       if constexpr (OP == kHidden) {
@@ -287,8 +303,9 @@ __device__ __forceinline__ void finish(const Args& p, const Tile& w, const float
   }
 }
 
-template <int OP, bool WIDE>
+template <int OP, bool WIDE, int BN, int SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) gated_tf32_kernel(const Args p) {
+  using C = Cfg<BN, SPLIT>;
   constexpr int kAlongK = WIDE ? kWide : kNarrow;
   constexpr int kWalkA = OP == kUp || OP == kDown ? kAlongK : kAcross;
   constexpr int kWalkB = OP == kWeight ? kAcross : kAlongK;
@@ -296,18 +313,23 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tf32_kernel(const Args p) {
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t base_addr = (raw_addr + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (base_addr - raw_addr);
-  uint8_t* aux = base + kStages * kStageBytes;
+  float* exchange = reinterpret_cast<float*>(base + C::kStages * C::kStageBytes);
+  uint8_t* aux = base + C::kStages * C::kStageBytes + C::kExchange;
   const uint32_t bars = smem_u32(aux);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(aux + kBarBytes);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(aux + kBarBytes + 4);
   int* prefix = reinterpret_cast<int*>(aux + kBarBytes + 16);
   int* seg = prefix + (MOE_MAX_EXPERTS + 1);
-  constexpr int S = kStages;
+  constexpr int S = C::kStages;
   auto full_bar = [&](int s) { return bars + 8u * s; };
   auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
   auto tfull_bar = [&](int a) { return bars + 8u * (2 * S + a); };
   auto tempty_bar = [&](int a) { return bars + 8u * (2 * S + 2 + a); };
   const uint32_t drain_bar = bars + 8u * (2 * S + 4);
+  const uint32_t sums_bar = bars + 8u * (2 * S + 5);  // SPLIT: every CTA's sums are in `exchange`
+  const uint32_t free_bar = bars + 8u * (2 * S + 6);  // and every CTA has read this one's
+  const int rank = SPLIT > 1 ? (int)cluster_ctarank() : 0;
+  const int first = (int)blockIdx.x / SPLIT, step = (int)gridDim.x / SPLIT;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -320,23 +342,33 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tf32_kernel(const Args p) {
       mbar_init(tempty_bar(a), kEpiWarps);
     }
     mbar_init(drain_bar, 1);
+    mbar_init(sums_bar, SPLIT * kEpiWarps);
+    mbar_init(free_bar, SPLIT * kEpiWarps);
     *abort_flag = 0;
     fence_barrier_init();
   }
   pdl_wait();
   if (warp == kLoadWarps) {
-    tmem_alloc(smem_u32(tmem_holder), kTmemCols);
+    tmem_alloc(smem_u32(tmem_holder), C::kTmemCols);
     tmem_relinquish();
   }
   if (OP != kWeight && warp == 0) {
     constexpr int feat = OP == kUp ? kBM / 2 : kBM;
-    build_tile_list(p, (p.n_out + feat - 1) / feat, prefix, seg, lane);
+    build_tile_list<BN>(p, (p.n_out + feat - 1) / feat, prefix, seg, lane);
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (SPLIT > 1) {
+    __syncwarp();
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  const int total = tile_count<OP>(p, prefix);
+  const int total = tile_count<OP, BN>(p, prefix);
+  // this CTA's K blocks of a tile
+  auto from = [&](const Tile& w) { return k_blocks<OP>(w) * rank / SPLIT; };
+  auto until = [&](const Tile& w) { return k_blocks<OP>(w) * (rank + 1) / SPLIT; };
 
   if (warp < kLoadWarps) {
     // ---------------------------------------------------------- loads and splits
@@ -345,31 +377,30 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tf32_kernel(const Args p) {
     uint32_t a_ok = 0, b_ok = 0;
     int64_t a_ld = 0, b_ld = 0;
     Tile w{};
-    int t = blockIdx.x, kb = 0, n_kb = 0, blocks1 = 0;
+    int t = first, kb = 0, n_kb = 0, blocks1 = 0;
+    bool in_tile = false;
     // makes (t, kb) the next K block there is; false if there is none
     auto settle = [&]() {
       while (t < total && kb >= n_kb) {
-        if (n_kb > 0) t += gridDim.x;
-        kb = n_kb = 0;
+        if (in_tile) t += step;
+        in_tile = true;
         if (t >= total) return false;
-        w = tile_at<OP>(p, t, prefix, seg);
-        n_kb = k_blocks<OP>(w);
+        w = tile_at<OP, BN>(p, t, prefix, seg);
+        kb = from(w);
+        n_kb = until(w);
         blocks1 = (w.K + kBK - 1) / kBK;
-        if (n_kb == 0) {
-          t += gridDim.x;
-          continue;
-        }
+        if (kb >= n_kb) continue;
         a_ok = b_ok = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           // rows of the A tile: features in order, for kUp 16 of the gate's and 16 of the up
           // projection's by turns
-          const int row = row_of<kWalkA>(tid, i);
+          const int row = row_of<kWalkA, kBM>(tid, i);
           if ((OP == kUp ? w.f0 + (row >> 5) * 16 + (row & 15) : w.f0 + row) < w.n_out)
             a_ok |= 1u << i;
-          if (row_of<kWalkB>(tid, i) < w.n_valid) b_ok |= 1u << i;
+          if (row_of<kWalkB, BN>(tid, i) < w.n_valid) b_ok |= 1u << i;
         }
-        const int row = row_of<kWalkA>(tid, 0), col = row_of<kWalkB>(tid, 0);
+        const int row = row_of<kWalkA, kBM>(tid, 0), col = row_of<kWalkB, BN>(tid, 0);
         if constexpr (OP == kUp) {
           a_at = (row & 16 ? p.a1 : p.a0) + ((int64_t)w.e * p.n_out + w.f0 + (row & 15)) * p.K;
         } else if constexpr (OP == kDown) {
@@ -390,17 +421,17 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tf32_kernel(const Args p) {
       }
       return t < total;
     };
-    auto load = [&](float (&a)[16], float (&b)[16]) {
+    auto load = [&](float (&a)[kBM / 8], float (&b)[BN / 8]) {
       // kInput's second product: the same places of the other operands
       const bool second = OP == kInput && kb >= blocks1;
       const int k0 = (kb - (second ? blocks1 : 0)) * kBK;
-      load_block<kWalkA>(a, second ? p.a1 + (a_at - p.a0) : a_at, (int64_t)(OP == kUp ? 16 : 32) * p.K, a_ok,
-                         a_ld, k0, w.K, kBM, tid);
-      load_block<kWalkB>(b, second ? p.b1 + (b_at - p.b0) : b_at, (int64_t)32 * p.K, b_ok, b_ld, k0, w.K, p.bn,
-                         tid);
+      load_block<kWalkA, kBM>(a, second ? p.a1 + (a_at - p.a0) : a_at, (int64_t)(OP == kUp ? 16 : 32) * p.K,
+                              a_ok, a_ld, k0, w.K, tid);
+      load_block<kWalkB, BN>(b, second ? p.b1 + (b_at - p.b0) : b_at, (int64_t)32 * p.K, b_ok, b_ld, k0, w.K,
+                             tid);
       ++kb;
     };
-    float av[16] = {}, bv[16] = {}, an[16] = {}, bn[16] = {};
+    float av[kBM / 8] = {}, bv[BN / 8] = {}, an[kBM / 8] = {}, bn[BN / 8] = {};
     int stage = 0;
     uint32_t phase = 0;
     bool have = settle();
@@ -409,9 +440,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tf32_kernel(const Args p) {
       const bool more = settle();
       if (more) load(an, bn);
       if (!mbar_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, p.status)) break;
-      uint8_t* to = base + stage * kStageBytes;
-      put_block<kWalkA>(av, to, kBM, tid);
-      put_block<kWalkB>(bv, to + 2 * kPartBytes, p.bn, tid);
+      uint8_t* to = base + stage * C::kStageBytes;
+      put_block<kWalkA, kBM>(av, to, tid);
+      put_block<kWalkB, BN>(bv, to + 2 * kAPart, tid);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full_bar(stage));
@@ -420,10 +451,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tf32_kernel(const Args p) {
         phase ^= 1u;
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        av[i] = an[i];
-        bv[i] = bn[i];
-      }
+      for (int i = 0; i < kBM / 8; ++i) av[i] = an[i];
+#pragma unroll
+      for (int i = 0; i < BN / 8; ++i) bv[i] = bn[i];
       have = more;
     }
   } else if (warp == kLoadWarps) {
@@ -432,37 +462,38 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tf32_kernel(const Args p) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        const Tile w = tile_at<OP>(p, t, prefix, seg);
-        const int n_kb = k_blocks<OP>(w);
+      for (int t = first; t < total && ok; t += step) {
+        const Tile w = tile_at<OP, BN>(p, t, prefix, seg);
+        const int kb0 = from(w), kb1 = until(w);
         // D fp32, A and B tf32, K-major, N = the tile's columns in groups of 16
         const uint32_t idesc = (1u << 4) | (2u << 7) | (2u << 10) |
                                ((uint32_t)(((w.n_valid + 15) & ~15) >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-        for (int kb = 0; kb < n_kb; ++kb) {
-          if (kb % kChunk == 0) {
+        for (int kb = kb0; kb < kb1; ++kb) {
+          const bool begins = (kb - kb0) % kChunk == 0;
+          if (begins) {
             if (!(ok = mbar_wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.status))) break;
             tc_fence_after();
           }
           if (!(ok = mbar_wait_bounded(full_bar(stage), phase, abort_flag, p.status))) break;
           tc_fence_after();
-          const uint32_t sa = base_addr + stage * kStageBytes;
-          const uint64_t a_hi = smem_desc_sw128(sa), a_lo = smem_desc_sw128(sa + kPartBytes);
-          const uint64_t b_hi = smem_desc_sw128(sa + 2 * kPartBytes);
-          const uint64_t b_lo = smem_desc_sw128(sa + 3 * kPartBytes);
-          const uint32_t d = tmem_base + (uint32_t)(acc * kAccCols);
-          const uint32_t first = kb % kChunk == 0 ? 0u : 1u;
+          const uint32_t sa = base_addr + stage * C::kStageBytes;
+          const uint64_t a_hi = smem_desc_sw128(sa), a_lo = smem_desc_sw128(sa + kAPart);
+          const uint64_t b_hi = smem_desc_sw128(sa + 2 * kAPart);
+          const uint64_t b_lo = smem_desc_sw128(sa + 2 * kAPart + C::kBPart);
+          const uint32_t d = tmem_base + (uint32_t)(acc * C::kAccCols);
+          const uint32_t more = begins ? 0u : 1u;
 #pragma unroll
           for (int kk = 0; kk < kBK / 8; ++kk) {
-            tc_mma_tf32(d, a_hi + 2 * kk, b_hi + 2 * kk, idesc, kk != 0 ? 1u : first);
-            tc_mma_tf32(d + kBN, a_lo + 2 * kk, b_hi + 2 * kk, idesc, kk != 0 ? 1u : first);
-            tc_mma_tf32(d + kBN, a_hi + 2 * kk, b_lo + 2 * kk, idesc, 1u);
+            tc_mma_tf32(d, a_hi + 2 * kk, b_hi + 2 * kk, idesc, kk != 0 ? 1u : more);
+            tc_mma_tf32(d + BN, a_lo + 2 * kk, b_hi + 2 * kk, idesc, kk != 0 ? 1u : more);
+            tc_mma_tf32(d + BN, a_hi + 2 * kk, b_lo + 2 * kk, idesc, 1u);
           }
           tc_commit(empty_bar(stage));
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
-          if (kb % kChunk == kChunk - 1 || kb == n_kb - 1) {
+          if ((kb - kb0) % kChunk == kChunk - 1 || kb == kb1 - 1) {
             tc_commit(tfull_bar(acc));
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
@@ -481,27 +512,27 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tf32_kernel(const Args p) {
     __syncwarp();
   } else {
     // ---------------------------------------------------------- epilogue: half of the columns each
-    const int quarter = warp & 3, c0 = (warp - kLoadWarps - 1) / 4 * 64;
+    const int quarter = warp & 3, c0 = (warp - kLoadWarps - 1) / 4 * C::kCols;
     int acc = 0;
-    uint32_t acc_phase = 0;
+    uint32_t acc_phase = 0, exchange_phase = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const Tile w = tile_at<OP>(p, t, prefix, seg);
-      const int chunks = (k_blocks<OP>(w) + kChunk - 1) / kChunk;
-      float s[64];
+    for (int t = first; t < total && ok; t += step) {
+      const Tile w = tile_at<OP, BN>(p, t, prefix, seg);
+      const int chunks = (until(w) - from(w) + kChunk - 1) / kChunk;
+      float s[C::kCols];
 #pragma unroll
-      for (int c = 0; c < 64; ++c) s[c] = 0.0f;
+      for (int c = 0; c < C::kCols; ++c) s[c] = 0.0f;
       for (int k = 0; k < chunks; ++k) {
         if (!(ok = mbar_wait_warp(tfull_bar(acc), acc_phase, abort_flag, p.status))) break;
         tc_fence_after();
-        const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kAccCols + c0);
+        const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * C::kAccCols + c0);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < C::kCols / 16; ++g) {
           if (c0 + g * 16 < w.n_valid) {
             uint32_t r[16];
 #pragma unroll
             for (int part = 1; part >= 0; --part) {
-              tmem_ld_32x32b_x16(taddr + (uint32_t)(part * kBN + g * 16), r);
+              tmem_ld_32x32b_x16(taddr + (uint32_t)(part * BN + g * 16), r);
               tmem_ld_wait16(r);
 #pragma unroll
               for (int c = 0; c < 16; ++c) s[g * 16 + c] += __uint_as_float(r[c]);
@@ -514,42 +545,120 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tf32_kernel(const Args p) {
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      if (ok && c0 < w.n_valid) finish<OP>(p, w, s, c0, quarter, lane);
+      if (!ok) break;
+      if constexpr (SPLIT == 1) {
+        if (c0 < w.n_valid) finish<OP, C::kCols>(p, w, s, c0, quarter, lane);
+      } else {
+        // [SPLIT senders][8 warps][kOwn columns][32 lanes] in the CTA that finishes the columns, once
+        // all have read the tile before's
+        if (!mbar_wait_cluster_warp(free_bar, exchange_phase ^ 1u, abort_flag, p.status)) break;
+        const int ew = warp - kLoadWarps - 1;
+        const uint32_t mine = smem_u32(exchange) + (uint32_t)((rank * kEpiWarps + ew) * C::kOwn * 32 + lane) * 4;
+#pragma unroll
+        for (int o = 0; o < SPLIT; ++o) {
+          const uint32_t to = cluster_addr(mine, o);
+#pragma unroll
+          for (int c = 0; c < C::kOwn; ++c)
+            st_cluster_u32(to + c * 128, __float_as_uint(s[o * C::kOwn + c]));
+        }
+        __syncwarp();
+        if (lane == 0)
+          for (int o = 0; o < SPLIT; ++o) mbar_arrive_cluster(cluster_addr(sums_bar, o));
+        if (!mbar_wait_cluster_warp(sums_bar, exchange_phase, abort_flag, p.status)) break;
+        float v[C::kOwn];
+#pragma unroll
+        for (int c = 0; c < C::kOwn; ++c) {
+          v[c] = 0.0f;
+#pragma unroll
+          for (int o = 0; o < SPLIT; ++o)
+            v[c] += exchange[((o * kEpiWarps + ew) * C::kOwn + c) * 32 + lane];
+        }
+        __syncwarp();
+        if (lane == 0)
+          for (int o = 0; o < SPLIT; ++o) mbar_arrive_cluster(cluster_addr(free_bar, o));
+        exchange_phase ^= 1u;
+        const int col = c0 + rank * C::kOwn;
+        if (col < w.n_valid) finish<OP, C::kOwn>(p, w, v, col, quarter, lane);
+      }
     }
   }
 
   tc_fence_before();
-  __syncthreads();
+  if constexpr (SPLIT > 1) {
+    __syncwarp();
+    cluster_sync();  // no store or arrive targets another CTA after this
+  } else {
+    __syncthreads();
+  }
   pdl_trigger();
   if (warp == kLoadWarps) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, kTmemCols);
+    tmem_dealloc(tmem_base, C::kTmemCols);
   }
 }
 
-template <int OP, bool WIDE>
-cudaError_t launch_walk(const Args& p, unsigned grid, cudaStream_t stream) {
+// Clusters of `split` CTAs, one CTA to an SM, that run at once: a few of those of four that the SMs
+// would make do not fit the device's groups of SMs (33 of 37).
+int64_t clusters_at_once(int split) {
+  return split == 1 ? num_sms() : std::max(1, num_sms() / split - 4);
+}
+
+template <int OP, bool WIDE, int BN, int SPLIT>
+cudaError_t launch_as(const Args& p, int64_t tiles, cudaStream_t stream) {
+  auto kern = gated_tf32_kernel<OP, WIDE, BN, SPLIT>;
+  constexpr int smem = Cfg<BN, SPLIT>::kSmemBytes;
   static int attr_done[64] = {0};  // per instantiation and device
-  const cudaError_t e = ensure_dynamic_smem(gated_tf32_kernel<OP, WIDE>, kSmemBytes, attr_done);
+  const cudaError_t e = ensure_dynamic_smem(kern, smem, attr_done);
   if (e != cudaSuccess) return e;
-  return launch_kernel(gated_tf32_kernel<OP, WIDE>, dim3(grid), dim3(kThreads), kSmemBytes, stream, p);
+  const unsigned clusters = (unsigned)std::min<int64_t>(tiles, clusters_at_once(SPLIT));
+  if constexpr (SPLIT == 1) return launch_kernel(kern, dim3(clusters), dim3(kThreads), smem, stream, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(clusters * SPLIT);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = SPLIT;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t l = cudaLaunchKernelEx(&cfg, kern, p);
+  count_launch();
+  return l;
+}
+
+template <int OP, bool WIDE>
+cudaError_t launch_walk(const Args& p, int64_t capacity_hint, cudaStream_t stream) {
+  // Rounds of tiles, as far as the host knows them, times a tile's K blocks; a block of 64 columns
+  // counts as 0.65 of one of 128 (A is most of the loads), the exchange of sums as three. Measured,
+  // tiles of 128, of 64, of 64 in clusters of four: 2048 rows, d 768, f 2048, down 88, 138, 180 us;
+  // 777 rows of 3 experts, d 321, f 1027, input 120, 90, 59 us; hidden 49, 32, 63 us.
+  auto over = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
+  const int64_t rows = std::max<int64_t>(1, std::min(capacity_hint, p.rows_max));
+  auto tiles = [&](int bn) -> int64_t {
+    if (OP == kWeight) return p.E * (over(p.f, kBM) * over(p.d, bn) + 2 * over(p.d, kBM) * over(p.f, bn));
+    return std::min<int64_t>(p.E, p.rows_max) * over(rows, bn) * over(p.n_out, OP == kUp ? kBM / 2 : kBM);
+  };
+  const int64_t blocks = (OP == kInput ? 2 : 1) * over(OP == kWeight ? rows : p.K, kBK);
+  const double t128 = (double)over(tiles(128), clusters_at_once(1)) * blocks;
+  const double t64 = over(tiles(64), clusters_at_once(1)) * 0.65 * blocks;
+  const double t64x4 = over(tiles(64), clusters_at_once(4)) * (0.65 * over(blocks, 4) + 3);
+  if (t64x4 < t128 && t64x4 < t64) return launch_as<OP, WIDE, 64, 4>(p, tiles(64), stream);
+  if (t64 < t128) return launch_as<OP, WIDE, 64, 1>(p, tiles(64), stream);
+  return launch_as<OP, WIDE, 128, 1>(p, tiles(128), stream);
 }
 
 template <int OP>
-cudaError_t launch(Args& p, int64_t capacity_hint, cudaStream_t stream) {
+cudaError_t launch(const Args& p, int64_t capacity_hint, cudaStream_t stream) {
   if (p.rows_max == 0) return cudaSuccess;
-  // tiles as far as the host knows
-  auto tiles = [&](int bn) -> int64_t {
-    auto over = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
-    if (OP == kWeight) return p.E * (over(p.f, kBM) * over(p.d, bn) + 2 * over(p.d, kBM) * over(p.f, bn));
-    const int64_t rows = std::max<int64_t>(1, std::min(capacity_hint, p.rows_max));
-    return std::min<int64_t>(p.E, p.rows_max) * over(rows, bn) * over(p.n_out, OP == kUp ? kBM / 2 : kBM);
-  };
-  p.bn = tiles(kBN) < num_sms() ? 64 : kBN;
   // K % 4 == 0: rows that are contiguous along k start on 16 bytes
-  const unsigned grid = (unsigned)std::min<int64_t>(tiles(p.bn), num_sms());
-  return OP != kWeight && p.K % 4 == 0 ? launch_walk<OP, OP != kWeight>(p, grid, stream)
-                                       : launch_walk<OP, false>(p, grid, stream);
+  if constexpr (OP != kWeight)
+    if (p.K % 4 == 0) return launch_walk<OP, true>(p, capacity_hint, stream);
+  return launch_walk<OP, false>(p, capacity_hint, stream);
 }
 
 Args args_of(const GatedFfn& g, int* status) {

@@ -445,3 +445,30 @@ def test_stream_of_no_such_device_is_refused(cuda_ok):
         moe.moe_gated_ffn(args_of(c), stream=Elsewhere())
     with pytest.raises(ValueError):
         moe.moe_grad_norm([c["x"]], stream=Elsewhere())
+
+
+@pytest.mark.parametrize("counts,d,f", [([700], 260, 1031), ([90, 0, 70, 100], 512, 1024),
+                                        ([3, 30, 0, 64, 65], 700, 301)], ids=str)
+def test_fp32_shapes_of_every_tile(cuda_ok, counts, d, f):
+    # tiles of 128 and of 64 rows and split sums, rows on and off 16-byte boundaries
+    c = make(len(counts), counts, d, f, torch.float32, seed=d, first=3)
+    got, kept = run(c, "gelu")
+    compare(c, got, "gelu", kept)
+
+
+def test_fp32_largest_and_smallest_factors(cuda_ok):
+    # the two-part split neither overflows near fp32's largest value nor loses small factors: with the
+    # rows and the weights of the first products scaled by inverse powers of two, every part of every
+    # factor scales with it (the least bits, below 2^-40 here, stay above 2^-126), so the results are
+    # the same bits
+    c = make(1, [20], 64, 64, torch.float32, bias=False, seed=25, slack=0)
+    clean = moe.moe_gated_ffn(args_of(c), train=True)["y_packed"].clone()
+    for scale in (2.0 ** 80, 2.0 ** -80):
+        e = dict(c, x=c["x"] / scale, w_gate=c["w_gate"] * scale, w_up=c["w_up"] * scale)
+        y = moe.moe_gated_ffn(args_of(e), train=True)["y_packed"]
+        assert torch.equal(y[:20], clean[:20]), scale
+    c["x"][0, 0] = torch.finfo(torch.float32).max
+    c["w_gate"][0, :, 0] = 2.0 ** -126
+    c["w_up"][0, :, 0] = 2.0 ** -126
+    h = moe.moe_gated_ffn(args_of(c), train=True)["h_packed"]
+    assert bool(torch.isfinite(h[0]).all())
