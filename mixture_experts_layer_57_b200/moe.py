@@ -592,24 +592,40 @@ def moe_layer_backward(args: LayerArgs, d_out: torch.Tensor, grads: dict, ws: to
 
 # ---------------------------------------------------------------- gated expert FFN
 
+_DTYPE_CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+# A decode step or a small model's training step takes some tens of microseconds on the GPU, so the
+# calls below look at their tensors in as few steps as they can.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _launch_on(dev: torch.device, stream):
-    """Where a call runs: the stream (default: the device's current one), and a context in which
-    that device is current and new tensors belong to that stream."""
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    if s.device != dev:
-        raise ValueError(f"a stream of {s.device} for tensors on {dev}")
-    if stream is None and dev.index == torch.cuda.current_device():
-        return s, contextlib.nullcontext()  # as it is already
+    """Where a call runs: the handle of the stream (default: the device's current one), and a
+    context in which that device is current and new tensors belong to that stream."""
+    if stream is None:
+        if dev.index == torch.cuda.current_device():  # as it is already
+            handle = (_raw_stream(dev.index) if _raw_stream is not None
+                      else torch.cuda.current_stream(dev).cuda_stream)
+            return handle, _HERE
+        stream = torch.cuda.current_stream(dev)
+    if stream.device != dev:
+        raise ValueError(f"a stream of {stream.device} for tensors on {dev}")
     ctx = contextlib.ExitStack()
     ctx.enter_context(torch.cuda.device(dev))
-    ctx.enter_context(torch.cuda.stream(s))
-    return s, ctx
+    ctx.enter_context(torch.cuda.stream(stream))
+    return stream.cuda_stream, ctx
 
 
-def _expect(name: str, t: torch.Tensor, like: torch.Tensor, shape: tuple, dtype=None):
-    if t.shape != shape or t.dtype != (dtype or like.dtype) or t.device != like.device:
-        raise ValueError(f"{name}: expected {tuple(shape)} {dtype or like.dtype} on {like.device}, got "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+_HERE = contextlib.nullcontext()
+
+
+def _expect(name: str, t: torch.Tensor, like: torch.Tensor, shape: tuple, dtype=None) -> int:
+    """The address of a tensor that has to be contiguous, of this shape and type, on like's device."""
+    if (t.shape != shape or t.dtype != (dtype or like.dtype) or t.get_device() != like.get_device()
+            or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous {tuple(shape)} {dtype or like.dtype} on "
+                         f"{like.device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
 
 
 def gated_ffn_args(x_packed: torch.Tensor, expert_offsets: torch.Tensor, w_gate: torch.Tensor,
@@ -621,27 +637,28 @@ def gated_ffn_args(x_packed: torch.Tensor, expert_offsets: torch.Tensor, w_gate:
     if act not in GATE_ACTS:
         raise ValueError(f"act must be one of {sorted(GATE_ACTS)}, got {act!r}")
     dt = _dt(x_packed)
+    if x_packed.dim() != 2 or w_gate.dim() != 3:
+        raise ValueError("x_packed must be [rows, d_model] and w_gate [E, d_ff, d_model]")
     E, d_ff, d = w_gate.shape
-    if x_packed.dim() != 2:
-        raise ValueError("x_packed must be [rows, d_model]")
+    rows = x_packed.shape[0]
     if rows_max is None:
-        rows_max = x_packed.shape[0]
-    if not 0 <= rows_max <= x_packed.shape[0]:
-        raise ValueError(f"rows_max {rows_max} is outside [0, {x_packed.shape[0]}]")
-    _expect("x_packed", x_packed, x_packed, (x_packed.shape[0], d))
-    _expect("expert_offsets", expert_offsets, x_packed, (E + 1,), torch.int32)
-    for name, t, shape in (("w_gate", w_gate, (E, d_ff, d)), ("w_up", w_up, (E, d_ff, d)),
-                           ("w_down", w_down, (E, d, d_ff)), ("b_gate", b_gate, (E, d_ff)),
-                           ("b_up", b_up, (E, d_ff)), ("b_down", b_down, (E, d))):
-        if t is not None:
-            _expect(name, t, x_packed, shape)
+        rows_max = rows
+    if not 0 <= rows_max <= rows:
+        raise ValueError(f"rows_max {rows_max} is outside [0, {rows}]")
+    x, up = x_packed, (E, d_ff, d)
     out = torch.float32 if out_dtype is None else out_dtype
-    if out not in (torch.float32, torch.bfloat16):
+    if out not in _DTYPE_CODES:
         raise ValueError(f"unsupported out_dtype {out}")
-    a = GatedFfnArgs(_ptr(x_packed), _ptr(expert_offsets), E, rows_max, d, d_ff, dt,
-                     MOE_BF16 if out == torch.bfloat16 else MOE_F32, GATE_ACTS[act], _ptr(w_gate),
-                     _ptr(b_gate), _ptr(w_up), _ptr(b_up), _ptr(w_down), _ptr(b_down),
-                     rows_max if capacity_hint is None else capacity_hint)
+    a = GatedFfnArgs(
+        _expect("x_packed", x, x, (rows, d)),
+        _expect("expert_offsets", expert_offsets, x, (E + 1,), torch.int32), E, rows_max, d, d_ff, dt,
+        _DTYPE_CODES[out], GATE_ACTS[act], _expect("w_gate", w_gate, x, up),
+        None if b_gate is None else _expect("b_gate", b_gate, x, (E, d_ff)),
+        _expect("w_up", w_up, x, up),
+        None if b_up is None else _expect("b_up", b_up, x, (E, d_ff)),
+        _expect("w_down", w_down, x, (E, d, d_ff)),
+        None if b_down is None else _expect("b_down", b_down, x, (E, d)),
+        rows_max if capacity_hint is None else capacity_hint)
     a.tensors = (x_packed, expert_offsets, w_gate, w_up, w_down, b_gate, b_up, b_down)
     return a
 
@@ -654,10 +671,10 @@ def moe_gated_ffn_backward_workspace_bytes(args: GatedFfnArgs) -> int:
     return _ws_bytes("moe_gated_ffn_backward_workspace_bytes", ctypes.byref(args))
 
 
-def _rows_of(name: str, t: torch.Tensor, x: torch.Tensor, rows: int, cols: int, dtype):
+def _rows_of(name: str, t: torch.Tensor, x: torch.Tensor, rows: int, cols: int, dtype) -> int:
     if t.dim() != 2 or t.shape[0] < rows:
         raise ValueError(f"{name} must be [at least {rows}, {cols}]")
-    _expect(name, t, x, (t.shape[0], cols), dtype)
+    return _expect(name, t, x, (t.shape[0], cols), dtype)
 
 
 def moe_gated_ffn(args: GatedFfnArgs, y_packed=None, h_packed=None, saved=None, train: bool = False,
@@ -671,21 +688,17 @@ def moe_gated_ffn(args: GatedFfnArgs, y_packed=None, h_packed=None, saved=None, 
     with ctx:
         if h_packed is None:
             h_packed = torch.empty(max(rows, 1), d_ff, dtype=dtype, device=dev)
-        else:
-            _rows_of("h_packed", h_packed, x, rows, d_ff, dtype)
         if y_packed is None:
             y_packed = torch.empty(max(rows, 1), d, dtype=out_dtype, device=dev)
-        else:
-            _rows_of("y_packed", y_packed, x, rows, d, out_dtype)
-        if saved is not None:
-            _expect("saved", saved, x, (2, rows, d_ff))
-        elif train:
+        if saved is None and train:
             saved = torch.empty(2, rows, d_ff, dtype=dtype, device=dev)
         if ws is None:
             ws = workspace(moe_gated_ffn_workspace_bytes(), dev)
         _check("moe_gated_ffn", lib().moe_gated_ffn(
-            ctypes.byref(args), _ptr(h_packed), _ptr(y_packed), _ptr(saved), _ptr(ws), ws.numel(),
-            s.cuda_stream))
+            ctypes.byref(args), _rows_of("h_packed", h_packed, x, rows, d_ff, dtype),
+            _rows_of("y_packed", y_packed, x, rows, d, out_dtype),
+            None if saved is None else _expect("saved", saved, x, (2, rows, d_ff)), _ptr(ws),
+            ws.numel(), s))
     return dict(y_packed=y_packed, h_packed=h_packed, saved=saved, ws=ws)
 
 
@@ -697,47 +710,42 @@ def moe_gated_ffn_backward(args: GatedFfnArgs, dy_packed: torch.Tensor, h_packed
     ``dx_dtype`` and the parameters' in ``grad_dtype`` (default fp32, as the layer's backward)."""
     x, _, w_gate, w_up, w_down, b_gate, b_up, b_down = args.tensors
     grads = {} if grads is None else grads
-    like = dict(dw_gate=w_gate, dw_up=w_up, dw_down=w_down, db_gate=b_gate, db_up=b_up,
-                db_down=b_down)
-    like = {n: t for n, t in like.items() if t is not None}
-    unknown = set(grads) - set(like) - {"dx_packed"}
-    if unknown:
-        raise ValueError(f"no such gradients: {sorted(unknown)}")
-    given = [t for n, t in grads.items() if n != "dx_packed" and t is not None]
+    like = {"dw_gate": w_gate, "dw_up": w_up, "dw_down": w_down}
+    for n, t in (("db_gate", b_gate), ("db_up", b_up), ("db_down", b_down)):
+        if t is not None:
+            like[n] = t
+    for n in grads:
+        if n not in like and n != "dx_packed":
+            raise ValueError(f"no such gradient: {n}")
+    get = grads.get
     if grad_dtype is None:
-        grad_dtype = given[0].dtype if given else torch.float32
+        grad_dtype = next((t.dtype for t in map(get, like) if t is not None), torch.float32)
+    dx = get("dx_packed")
     if dx_dtype is None:
-        dx_dtype = grads["dx_packed"].dtype if grads.get("dx_packed") is not None else x.dtype
-    rows = args.rows_max
-    s, ctx = _launch_on(x.device, stream)
+        dx_dtype = x.dtype if dx is None else dx.dtype
+    dev, rows, d, d_ff = x.device, args.rows_max, args.d_model, args.d_ff
+    s, ctx = _launch_on(dev, stream)
     with ctx:
-        _rows_of("dy_packed", dy_packed, x, rows, args.d_model, x.dtype)
-        _rows_of("h_packed", h_packed, x, rows, args.d_ff, x.dtype)
-        _expect("saved", saved, x, (2, rows, args.d_ff))
-        if grads.get("dx_packed") is None:
-            grads["dx_packed"] = torch.empty(max(rows, 1), args.d_model, dtype=dx_dtype,
-                                             device=x.device)
-        else:
-            _rows_of("dx_packed", grads["dx_packed"], x, rows, args.d_model, dx_dtype)
+        if dx is None:
+            dx = grads["dx_packed"] = torch.empty(max(rows, 1), d, dtype=dx_dtype, device=dev)
+        g = GatedFfnGrads(dx_packed=_rows_of("dx_packed", dx, x, rows, d, dx_dtype),
+                          dx_dtype=_dt(dx))
         for n, t in like.items():
-            if grads.get(n) is None:
-                grads[n] = torch.empty(t.shape, dtype=grad_dtype, device=x.device)
-            else:
-                _expect(n, grads[n], x, t.shape, grad_dtype)
+            o = get(n)
+            if o is None:
+                o = grads[n] = torch.empty(t.shape, dtype=grad_dtype, device=dev)
+            setattr(g, n, _expect(n, o, x, t.shape, grad_dtype))
+        g.grad_dtype = _dt(grads["dw_gate"])
         if ws is None:
-            ws = workspace(moe_gated_ffn_backward_workspace_bytes(args), x.device)
-        g = GatedFfnGrads(**{n: _ptr(t) for n, t in grads.items()}, dx_dtype=_dt(grads["dx_packed"]),
-                          grad_dtype=_dt(grads["dw_gate"]))
+            ws = workspace(moe_gated_ffn_backward_workspace_bytes(args), dev)
         _check("moe_gated_ffn_backward", lib().moe_gated_ffn_backward(
-            ctypes.byref(args), _ptr(dy_packed), _ptr(h_packed), _ptr(saved), ctypes.byref(g),
-            _ptr(ws), ws.numel(), s.cuda_stream))
+            ctypes.byref(args), _rows_of("dy_packed", dy_packed, x, rows, d, x.dtype),
+            _rows_of("h_packed", h_packed, x, rows, d_ff, x.dtype),
+            _expect("saved", saved, x, (2, rows, d_ff)), ctypes.byref(g), _ptr(ws), ws.numel(), s))
     return grads
 
 
 # ---------------------------------------------------------------- gradient norm and clipping
-
-_GRAD_CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
-
 
 def _grad_list(grads, out=None):
     """The tensors as an array of ``moe_grad_tensor`` (host memory), their number and device."""
@@ -757,7 +765,7 @@ def _grad_list(grads, out=None):
     if sizes[:n] != sizes[-n:]:
         raise ValueError("every output must have its gradient's size")
     try:
-        codes = [_GRAD_CODES[t.dtype] for t in tensors]
+        codes = [_DTYPE_CODES[t.dtype] for t in tensors]
     except KeyError as e:
         raise ValueError(f"unsupported dtype {e.args[0]}") from None
     words = array.array("q", bytes(32 * n))  # four 64-bit words a tensor
@@ -784,8 +792,7 @@ def _grad_norm(table, n, dev, norm, ws, s):
         _check_norm(norm, dev)
     if ws is None:
         ws = workspace(moe_grad_norm_workspace_bytes(), dev)
-    _check("moe_grad_norm", lib().moe_grad_norm(table, n, norm.data_ptr(), _ptr(ws), ws.numel(),
-                                                s.cuda_stream))
+    _check("moe_grad_norm", lib().moe_grad_norm(table, n, norm.data_ptr(), _ptr(ws), ws.numel(), s))
     return norm
 
 
@@ -805,8 +812,7 @@ def moe_clip_grads(grads, norm: torch.Tensor, max_norm: float, out=None, stream=
     _check_norm(norm, dev)
     s, ctx = _launch_on(dev, stream)
     with ctx:
-        _check("moe_clip_grads", lib().moe_clip_grads(table, n, norm.data_ptr(), max_norm,
-                                                      s.cuda_stream))
+        _check("moe_clip_grads", lib().moe_clip_grads(table, n, norm.data_ptr(), max_norm, s))
     return grads if out is None else out
 
 
@@ -817,8 +823,7 @@ def moe_clip_grad_norm(grads, max_norm: float, out=None, norm=None, ws=None,
     s, ctx = _launch_on(dev, stream)
     with ctx:
         norm = _grad_norm(table, n, dev, norm, ws, s)
-        _check("moe_clip_grads", lib().moe_clip_grads(table, n, norm.data_ptr(), max_norm,
-                                                      s.cuda_stream))
+        _check("moe_clip_grads", lib().moe_clip_grads(table, n, norm.data_ptr(), max_norm, s))
     return norm
 
 
