@@ -70,12 +70,17 @@ struct GemmMaps {
 //   kPair    two CTAs on two SMs, MMAs of M = 256 (cta_group::2): each holds 128 A rows, half of
 //            the token rows and its half of the accumulator, so each token row is loaded once per
 //            pair
-//   kSplit   a cluster of S = 1, 2, 4 or 8 CTAs, each with its share of the K blocks; each CTA then
+//   kSplit   a cluster of S = 1 to 8 CTAs, each with its share of the K blocks; each CTA then
 //            finishes every S-th group of 16 tokens, for which the others write their partial sums
 //            into its shared memory
 enum Mode { kPair = 0, kSplit = 1 };
 constexpr int kMaxSplit = 8;
 constexpr int kPartChunk = 16 * kBM * 4;  // partial sums of 16 tokens
+constexpr int kPartChunks = 7;
+// Partial sums that a CTA receives for one tile of `bn` tokens, in groups of 16.
+__host__ __device__ constexpr int parts_of(int bn, int width) {
+  return (width - 1) * ((bn / 16 + width - 1) / width);
+}
 
 // FT: A tiles of 128 rows per CTA tile, each with its own accumulator, that share the token rows
 // of a stage. Two sets of accumulators: a tile's MMAs run while the one before is finished.
@@ -88,9 +93,7 @@ struct GemmCfg {
   static constexpr int kABytes = FT * kBM * kBK * 2;
   static constexpr int kBRows = MODE == kPair ? BN / 2 : BN;   // token rows per CTA and stage
   static constexpr int kStageBytes = kABytes + kBRows * kBK * 2;
-  // kSplit: the other CTAs' sums for this one's groups of 16 tokens, of which a tile has at most
-  // eight: seven of one group for S = 8, three of two for 4, one of four for 2
-  static constexpr int kPartBytes = MODE == kSplit ? (kMaxSplit - 1) * kPartChunk : 0;
+  static constexpr int kPartBytes = MODE == kSplit ? kPartChunks * kPartChunk : 0;
   static constexpr int kStagesFit = (kRingBytes - kPartBytes) / kStageBytes;
   static constexpr int kStages = kStagesFit > 12 ? 12 : kStagesFit;
   static constexpr int kAccCols = FT * BN;
@@ -647,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t taddr = d_tmem + ((uint32_t)(quarter * 32) << 16);
         const int groups = sh.groups(BN);
         for (int g = set; g * 16 < tl.n_valid; g += kEpiSets) {
-          const int owner = g & (width - 1);  // the width is a power of two
+          const int owner = g % width;
           if (owner == rank) continue;
           const int slot = (rank < owner ? rank : rank - 1) * groups + g / width;
           const uint32_t to = cluster_addr(smem_u32(part), owner) +
@@ -661,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0)
           for (int s = 1; s < width; ++s)
-            mbar_arrive_cluster(cluster_addr(B.part_full(), (rank + s) & (width - 1)));
+            mbar_arrive_cluster(cluster_addr(B.part_full(), (rank + s) % width));
         if (!mbar_wait_cluster_warp(B.part_full(), part_phase, abort_flag, p.status)) break;
       }
       epilogue<OP, BN, FT, MODE>(tl, f0, p, d_tmem, quarter, set, lane, st, sh, in);
@@ -669,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0)
           for (int s = 1; s < width; ++s)
-            mbar_arrive_cluster(cluster_addr(B.part_free(), (rank + s) & (width - 1)));
+            mbar_arrive_cluster(cluster_addr(B.part_free(), (rank + s) % width));
       }
       part_phase ^= 1u;
       // one arrival per warp: the barrier takes arrivals one after another
@@ -759,11 +762,11 @@ cudaError_t config_of(int width, Config* c) {
   static int attr_done[64] = {0};  // per instantiation and device
   cudaError_t e = ensure_dynamic_smem(c->kern, c->smem, attr_done);
   if (e != cudaSuccess) return e;
-  static std::atomic<int> slots[64][4];
+  static std::atomic<int> slots[64][kMaxSplit + 1];
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  std::atomic<int>& cached = slots[dev][width == 8 ? 3 : width / 2];
+  std::atomic<int>& cached = slots[dev][width];
   if ((c->slots = cached.load(std::memory_order_relaxed)) == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)width);
@@ -811,8 +814,8 @@ cudaError_t config_of(int bn, int ft, int mode, int width, Config* c) {
 //   - for more rows pairs with one A tile and 256 token columns (TMEM holds two sets of
 //     accumulators only of one such tile; 128 rows an expert on average, 160 at most, up: 429 us;
 //     two A tiles and one set, the epilogue not overlapped, 480);
-//   - splits where tiles are fewer than SMs (8 rows, d 8192 -> 2048: 19 us in clusters of 4, 27 of 2,
-//     44 unsplit).
+//   - splits where tiles are fewer than SMs (8 rows, d 8192 -> 2048, weights cold: 18.8 us in clusters
+//     of 6, 19.5 of 4, 25.5 of 2, 27.7 of 8, of which only 15 of 16 fit at once, 44 unsplit).
 template <int OP>
 cudaError_t launch_op(const GemmMaps& m, const GemmParams& p, int64_t capacity_hint,
                       cudaStream_t stream) {
@@ -851,8 +854,9 @@ cudaError_t launch_op(const GemmMaps& m, const GemmParams& p, int64_t capacity_h
   if (fit <= 128) e = consider(fit, 2, kPair, 2);
   if (e == cudaSuccess) e = consider(fit, 1, kPair, 2);
   if (fit == 256 && e == cudaSuccess) e = consider(128, 1, kPair, 2);
-  for (int width = 1; width <= kMaxSplit && n_blocks >= 4 * width; width *= 2)
-    if (e == cudaSuccess) e = consider(std::min(fit, 128), 1, kSplit, width);
+  for (int width = 1; width <= kMaxSplit && n_blocks >= 4 * width; ++width)
+    if (e == cudaSuccess && parts_of(std::min(fit, 128), width) <= kPartChunks)
+      e = consider(std::min(fit, 128), 1, kSplit, width);
   if (e != cudaSuccess) return e;
   return launch_clusters(best, best_tiles, stream, m, p);
 }
