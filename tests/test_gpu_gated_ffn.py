@@ -472,3 +472,53 @@ def test_fp32_largest_and_smallest_factors(cuda_ok):
     c["w_up"][0, :, 0] = 2.0 ** -126
     h = moe.moe_gated_ffn(args_of(c), train=True)["h_packed"]
     assert bool(torch.isfinite(h[0]).all())
+
+
+def test_fp32_many_experts(cuda_ok):
+    counts = [(5 * i) % 4 for i in range(1024)]
+    c = make(1024, counts, 33, 17, torch.float32, seed=26)
+    got, kept = run(c, "silu")
+    compare(c, got, "silu", kept)
+
+
+def test_few_rows_of_many_experts(cuda_ok):
+    counts = [0] * 1024
+    counts[0], counts[517], counts[1023] = 2, 1, 3
+    c = make(1024, counts, 33, 17, torch.float32, seed=27, slack=0)
+    y = moe.moe_gated_ffn(args_of(c))["y_packed"]
+    a = 0
+    for e in (0, 517, 1023):
+        n = counts[e]
+        params = {k: c[k][e] for k in NAMES}
+        gated_ref.check("y", y[a:a + n], *gated_ref.segment(c["x"][a:a + n], params, "silu")["y"])
+        a += n
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_one_long_segment(cuda_ok, dtype):
+    c = make(3, [3, 70_001, 20], 40, 24, dtype, seed=28)
+    got, kept = run(c, "gelu")
+    compare(c, got, "gelu", kept)
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 64), (torch.float32, 17)], ids=str)
+def test_hidden_tensors_past_32_bit_offsets(cuda_ok, dtype, d):
+    # h, saved, dg and du have more than 2^31 elements; the last expert lies behind that
+    rows, last, f = 262_300, 100, 8192
+    c = make(2, [rows, last], d, f, dtype, bias=False, seed=29, slack=0)
+    assert (rows + last) * f > 2 ** 31 and rows * f > 2 ** 31
+    args = args_of(c)
+    r = moe.moe_gated_ffn(args, train=True)
+    g = moe.moe_gated_ffn_backward(args, c["dy"], r["h_packed"], r["saved"], grad_dtype=dtype)
+    ref = gated_ref.segment(c["x"][rows:], {k: None if c[k] is None else c[k][1] for k in NAMES}, "silu",
+                            c["dy"][rows:])
+    gated_ref.check("y", r["y_packed"][rows:], *ref["y"])
+    gated_ref.check("dx", g["dx_packed"][rows:], *ref["dx_packed"])
+    for k in ("w_gate", "w_up", "w_down"):
+        gated_ref.check("d" + k, g["d" + k][1], *ref["d" + k])
+    # and rows on both sides of the border, of the first expert
+    at = 2 ** 31 // f - 20
+    ref = gated_ref.segment(c["x"][at:at + 40], {k: None if c[k] is None else c[k][0] for k in NAMES}, "silu",
+                            c["dy"][at:at + 40])
+    gated_ref.check("y", r["y_packed"][at:at + 40], *ref["y"])
+    gated_ref.check("dx", g["dx_packed"][at:at + 40], *ref["dx_packed"])

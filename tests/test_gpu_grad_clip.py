@@ -163,3 +163,15 @@ def test_places_of_any_relative_alignment(cuda_ok, src, dst):
             check(grads, 0.5, out=[s[b:b + n] for s, n in zip(space, sizes)])
             for s, n in zip(space, sizes):
                 assert bool((s[:b] == 77.0).all()) and bool((s[b + n:] == 77.0).all())
+
+
+def test_tensor_past_32_bit_offsets(cuda_ok):
+    n = 2 ** 31 + 9
+    g = torch.full((n,), 0.5, dtype=torch.bfloat16, device="cuda")
+    g[0], g[-1] = 4.0, -8.0
+    want = ((n - 2) * 0.25 + 16 + 64) ** 0.5
+    norm = moe.moe_clip_grad_norm([g], want / 2)
+    assert abs(norm.item() - want) <= NORM_TOL * want
+    # the factor is 1/2 within a few 2^-24, and bf16 rounds these products to exact halves
+    assert g[0].item() == 2.0 and g[-1].item() == -4.0
+    assert g[1].item() == 0.25 and bool((g[-1000:-1] == 0.25).all()) and bool((g[2 ** 31 - 500:2 ** 31] == 0.25).all())
