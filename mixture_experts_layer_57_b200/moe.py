@@ -398,6 +398,12 @@ def moe_grouped_gemm(x_packed: torch.Tensor, expert_offsets: torch.Tensor, w: to
 
 def moe_combine(y_packed: torch.Tensor, expert_offsets, expert_ids, slot, gates, residual=None,
                 dense=None, out=None, out_dtype=None, rows_max=None, ws=None, stream=None) -> dict:
+    """The gate-weighted sum of each token's expert rows. ``y_packed``, ``gates`` and ``dense`` are
+    read as fp32; experts and dense blocks that write bf16 (moe_gated_ffn with a bf16 ``out_dtype``)
+    cannot be combined."""
+    for name, t in (("y_packed", y_packed), ("gates", gates), ("dense", dense)):
+        if t is not None and t.dtype != torch.float32:
+            raise ValueError(f"{name} must be torch.float32, got {t.dtype}")
     T, k = expert_ids.shape
     d = y_packed.shape[1]
     E = expert_offsets.shape[0] - 1
