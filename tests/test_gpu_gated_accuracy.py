@@ -1,0 +1,63 @@
+"""Accuracy of the gated FFN's activations where the element-wise bounds of whole products are too
+wide to tell: pre-activations are set exactly through the biases (all weights of the first products are
+zero), so the kept tensors and h show the activation alone."""
+import math
+
+import pytest
+import torch
+
+from mixture_experts_layer_57_b200 import moe
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+def block(z, zu, dtype, act, rows=9, train=True):
+    """One dense block whose rows all have the pre-activations z and zu [f]: h and the saved planes."""
+    f, d = z.numel(), 8
+    zero = torch.zeros(1, f, d, dtype=dtype, device="cuda")
+    x = torch.ones(rows, d, dtype=dtype, device="cuda")
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    args = moe.gated_ffn_args(x, off, zero, zero, torch.zeros(1, d, f, dtype=dtype, device="cuda"),
+                              b_gate=z.to(dtype)[None].cuda(), b_up=zu.to(dtype)[None].cuda(), act=act)
+    r = moe.moe_gated_ffn(args, train=train)
+    h = r["h_packed"]
+    assert all(torch.equal(h[0], h[i]) for i in range(rows))
+    return h[0].double().cpu(), None if r["saved"] is None else r["saved"][:, rows - 1].cpu()
+
+
+def exact(z, act):
+    """act(z) and act'(z) in 64 bits without cancellation, with bounds on the relative error of an fp32
+    evaluation. GeLU: the argument of erfc is off by 1.3 2^-24 of itself (a product and the constant),
+    which erfc magnifies by at most z^2 + 1; erfc itself by 4 units (8 2^-24), the exponential of the
+    density by 2 units after z^2 / 2 2^-24 from its argument; products and sums 2^-24 each. SiLU: the
+    exponential, an addition, a division and a product."""
+    z = z.double()
+    if act == "gelu":
+        cdf = 0.5 * torch.special.erfc(-z / math.sqrt(2))
+        pdf = torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        rc = ((z * z + 2) * 1.3 + 9) * U
+        return (z * cdf, z.abs() * cdf * (rc + U), cdf + z * pdf,
+                cdf * rc + (z * pdf).abs() * (z * z / 2 + 7) * U + (cdf + z * pdf).abs() * U)
+    s = torch.sigmoid(z)
+    t = 1 + z * torch.sigmoid(-z)
+    return (z * s, 8 * U * (z * s).abs(), s * t,
+            s * (z.abs() * (6 * s + 2 * torch.sigmoid(-z)) + 8 * t.abs()) * U)
+
+
+def assert_within(got, want, bound, what):
+    err = (got - want).abs()
+    i = int((err / bound).argmax())
+    assert bool((err <= bound).all()), f"{what}: {float(err[i]):.3g} of {float(want[i]):.6g}, " \
+                                       f"{float(err[i] / bound[i]):.3g} times the bound, at {i}"
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_fp32_activation_and_derivative(cuda_ok, act):
+    z = torch.linspace(-8, 8, 2049)
+    a, ea, da, eda = exact(z, act)
+    one = torch.ones_like(z)
+    h, saved = block(z, one, torch.float32, act)
+    for got in (h, saved[0].double(), block(z, one, torch.float32, act, rows=3, train=False)[0]):
+        assert_within(got, a, ea + 2.0 ** -140, "act")
+    assert_within(saved[1].double(), da, eda + 2.0 ** -140, "act'")
