@@ -61,3 +61,13 @@ def test_fp32_activation_and_derivative(cuda_ok, act):
     for got in (h, saved[0].double(), block(z, one, torch.float32, act, rows=3, train=False)[0]):
         assert_within(got, a, ea + 2.0 ** -140, "act")
     assert_within(saved[1].double(), da, eda + 2.0 ** -140, "act'")
+
+
+@pytest.mark.parametrize("act,far", [("silu", 80.0), ("gelu", 12.5)])
+def test_bf16_activation(cuda_ok, act, far):
+    # h is act(z) rounded once: half a step, and what the approximate exponential adds (its error is
+    # 2 + 1.2 |argument| units, the argument's own rounding |argument| units: 2^-15 at either end here)
+    z = torch.linspace(-far, far, 4096).to(torch.bfloat16).float()
+    a = exact(z, act)[0]
+    h, _ = block(z, torch.ones_like(z), torch.bfloat16, act)
+    assert_within(h, a, (2.0 ** -8 + 2.0 ** -14) * a.abs() + 2.0 ** -133, "act")
