@@ -215,8 +215,9 @@ __device__ __forceinline__ void load_block(float (&v)[R / 8], const float* at, i
 }
 
 // hi: x rounded to 11 bits (tf32), lo: the exact rest, rounded to 11. Where one of the four is 2^127
-// or more, infinite or NaN, hi is cut instead: it neither overflows nor loses a NaN. An infinite x may
-// make NaN of its sums (with a zero lo of the other factor).
+// or more, infinite or NaN, both are cut instead: hi does not overflow, and of a NaN, whose payload may
+// be cut from hi, x - hi is a NaN that lo keeps (rounding up would carry it into -0). x - hi is NaN for
+// an infinite x too, so its sums are NaN. (A NaN made quiet in hi: 132 us for 108, 1000 rows below.)
 __device__ __forceinline__ void split4(const float* x, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
   float m = fabsf(x[0]);
 #pragma unroll
@@ -225,7 +226,7 @@ __device__ __forceinline__ void split4(const float* x, uint32_t (&hi)[4], uint32
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     hi[j] = (__float_as_uint(x[j]) + half) & 0xffffe000u;
-    lo[j] = (__float_as_uint(x[j] - __uint_as_float(hi[j])) + 0x1000u) & 0xffffe000u;
+    lo[j] = (__float_as_uint(x[j] - __uint_as_float(hi[j])) + half) & 0xffffe000u;
   }
 }
 

@@ -71,3 +71,17 @@ def test_bf16_activation(cuda_ok, act, far):
     a = exact(z, act)[0]
     h, _ = block(z, torch.ones_like(z), torch.bfloat16, act)
     assert_within(h, a, (2.0 ** -8 + 2.0 ** -14) * a.abs() + 2.0 ** -133, "act")
+
+
+def test_fp32_nan_of_any_payload(cuda_ok):
+    # NaNs whose payload lies in the low bits only: the two-part split may not turn them into infinities
+    # (second parts of the weights have the first ones' sign, so infinities would not cancel)
+    for bits in (0x7f800001, 0x7f801fff, 0x7fc00000, 0x7fffffff, -1, -0x7fffff):
+        x = torch.zeros(20, 32, device="cuda")
+        x.view(torch.int32)[4, 7] = bits
+        w = torch.full((1, 32, 32), 1 + 2.0 ** -13, device="cuda")
+        args = moe.gated_ffn_args(x, torch.tensor([0, 20], dtype=torch.int32, device="cuda"), w, w, w)
+        r = moe.moe_gated_ffn(args, train=True)
+        for t in (r["h_packed"], r["y_packed"], r["saved"][0]):
+            assert bool(torch.isnan(t[4]).all()), hex(bits & 0xffffffff)
+            assert bool((t[:4] == 0).all()) and bool((t[5:] == 0).all())
