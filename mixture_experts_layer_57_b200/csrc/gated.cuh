@@ -49,21 +49,23 @@ __device__ __forceinline__ void gate_act(float z, int act, float& a, float& da) 
 }
 
 // Eight values in 8 x 16 bits with one exponent between them (what the forward pass of a bf16
-// layer keeps for the backward pass): each is rounded to fp16 after scaling by the power of two
-// that brings the largest magnitude into [1/2, 1), which leaves bit 14 of every fp16 zero; there
-// the eight bits of the exponent go, one each. Values within 2^-13 of the largest keep 11 bits
-// where bf16 keeps 8 (plain bf16 copies of these two tensors raised the error of the weight
-// gradients by a fifth), smaller ones an absolute error of 2^-25 of the largest. Where a magnitude
-// is 2^126 or more, infinite or NaN, the exponent is 255 and every value is the sign, the exponent
-// and six bits of mantissa of its fp32 form.
+// layer keeps for the backward pass): each is rounded to fp16 after scaling by the power of two, of
+// even exponent, that brings the largest magnitude into [1/4, 1), which leaves bit 14 of every fp16
+// zero; there go the eight bits of a code, one each. Bits 0..6 of it are half the exponent. Values
+// within 2^-12 of the largest keep 11 bits where bf16 keeps 8 (plain bf16 copies of these two tensors
+// raised the error of the weight gradients by a fifth), smaller ones an error of up to 2^-25 at that
+// scale, which is bf16's half step at 2^-17. Where a value other than zero lies below 2^-17 there, all
+// eight are scaled bf16 instead (bit 7 of the code; bit 14 of a bf16 below 1 is zero too): a gate that is
+// shut beside one wide open keeps its 8 bits. Where a magnitude is 2^126 or more, infinite or NaN, bits
+// 0..6 are all set and every value is the sign, the exponent and six bits of mantissa of its fp32 form.
 __device__ __forceinline__ uint4 pack_block8(const float (&v)[8]) {
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(fabsf(v[i])));
-  const uint32_t e = __float_as_uint(m) >> 23;
+  const uint32_t half = ((__float_as_uint(m) >> 23) + 1u) >> 1;
   uint32_t w[4];
-  if (e >= 253u) {
+  if (half >= 127u) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t h[2];
@@ -71,29 +73,40 @@ __device__ __forceinline__ uint4 pack_block8(const float (&v)[8]) {
       for (int j = 0; j < 2; ++j) {
         uint32_t u = __float_as_uint(v[2 * i + j]);
         if ((u & 0x7fffffffu) > 0x7f800000u) u |= 0x00400000u;  // a NaN stays one when cut
-        h[j] = ((u >> 16) & 0x8000u) | 0x4000u | ((u >> 17) & 0x3fffu);
+        h[j] = ((u >> 16) & 0x8000u) | ((u >> 17) & 0x3fffu);
       }
       w[i] = h[0] | (h[1] << 16);
     }
   } else {
-    const float scale = __uint_as_float((253u - e) << 23);  // 2^(126 - e)
-    const uint32_t bits = (e & 15u) | ((e >> 4) << 16);
+    const float scale = __uint_as_float((253u - 2u * half) << 23);  // 2^(126 - 2 half)
+    float s[8], least = 1.0f;  // the smallest magnitude other than zero
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s[i] = v[i] * scale;
+      least = fminf(least, v[i] != 0.0f ? fabsf(s[i]) : 1.0f);
+    }
+    const bool wide = least < 0x1p-17f;
+    const uint32_t code = half | (wide ? 0x80u : 0u);
+    const uint32_t bits = (code & 15u) | ((code >> 4) << 16);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t h;
-      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(v[2 * i + 1] * scale), "f"(v[2 * i] * scale));
+      if (wide) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(s[2 * i + 1]), "f"(s[2 * i]));
+      else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(s[2 * i + 1]), "f"(s[2 * i]));
       w[i] = h | (((bits >> i) << 14) & 0x40004000u);
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  // code 127
+  return make_uint4(w[0] | 0x40004000u, w[1] | 0x40004000u, w[2] | 0x40004000u, w[3] | 0x00004000u);
 }
 __device__ __forceinline__ void unpack_block8(const uint4& q, float (&v)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
   uint32_t bits = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) bits |= ((w[i] & 0x40004000u) >> 14) << i;
-  const uint32_t e = (bits | (bits >> 12)) & 0xffu;
-  if (e == 255u) {
+  const uint32_t code = (bits | (bits >> 12)) & 0xffu, half = code & 0x7fu;
+  if (half == 127u) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -102,11 +115,12 @@ __device__ __forceinline__ void unpack_block8(const uint4& q, float (&v)[8]) {
         v[2 * i + j] = __uint_as_float(((h & 0x8000u) << 16) | ((h & 0x3fffu) << 17));
       }
   } else {
-    const float scale = __uint_as_float((e + 1u) << 23);  // 2^(e - 126)
+    const float scale = __uint_as_float((2u * half + 1u) << 23);  // 2^(2 half - 126)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t x = w[i] & 0xbfffbfffu;
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+      float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+      if (code & 0x80u) f = make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
       v[2 * i] = f.x * scale;
       v[2 * i + 1] = f.y * scale;
     }

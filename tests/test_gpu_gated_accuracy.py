@@ -73,6 +73,72 @@ def test_bf16_activation(cuda_ok, act, far):
     assert_within(h, a, (2.0 ** -8 + 2.0 ** -14) * a.abs() + 2.0 ** -133, "act")
 
 
+def unpack(saved):
+    """Eight neighbours of 16 bits with their shared code in bit 14 of each: bits 0..6 of it are half
+    the exponent (rounded up), bit 7 says bf16 instead of fp16; 127: the top bits of each value itself."""
+    w = saved.view(torch.int16).to(torch.int32).reshape(-1, 8) & 0xffff
+    flag = (w >> 14) & 1
+    code = sum(flag[:, 2 * i] << i | flag[:, 2 * i + 1] << (4 + i) for i in range(4))
+    w = w & 0xbfff
+    half, wide = code & 127, (code >> 7) == 1
+    as16 = lambda t: torch.where(t >= 2 ** 15, t - 2 ** 16, t).to(torch.int16)  # noqa: E731
+    fp16 = as16(w).view(torch.float16).double()
+    bf16 = as16(w).view(torch.bfloat16).double()
+    own = ((w & 0x8000) << 16 | (w & 0x3fff) << 17)
+    own = torch.where(own >= 2 ** 31, own - 2 ** 32, own).to(torch.int32).view(torch.float32).double()
+    v = torch.where(wide[:, None], bf16, fp16) * torch.exp2(2.0 * half - 126)[:, None].double()
+    return torch.where((half == 127)[:, None], own, v).reshape(-1)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_saved_tensors_keep_eleven_bits(cuda_ok, act):
+    gen = torch.Generator().manual_seed(1)
+    z = (2 * torch.randn(4096, generator=gen)).to(torch.bfloat16).float()
+    zu = torch.randn(4096, generator=gen).to(torch.bfloat16).float()
+    a, _, da, _ = exact(z, act)
+    q = zu.double() * da
+    _, saved = block(z, zu, torch.bfloat16, act)
+    for got, want, slack, what in ((unpack(saved[0]), a, 2.0 ** -16 * a.abs(), "act"),
+                                   (unpack(saved[1]), q, 2.0 ** -18 * zu.double().abs(), "zu act'")):
+        most = want.abs().reshape(-1, 8).max(1, keepdim=True).values.expand(-1, 8).reshape(-1)
+        # half a step of 11 bits; values far below the block's largest: half of fp16's least step at a
+        # scale that is at most four times the largest
+        bound = 2.0 ** -11 * want.abs() + 2.0 ** -23 * most + slack
+        # a block with a value below 2^-17, at a scale where its largest is 1/4 to 1, keeps 8 bits of each:
+        # so may those with a ratio below 2^-15 (of GeLU gates this far out one in six)
+        least = want.abs().reshape(-1, 8).min(1, keepdim=True).values.expand(-1, 8).reshape(-1)
+        few = least < 2.0 ** -15 * most
+        bound = torch.where(few, 2.0 ** -8 * want.abs() + slack, bound)
+        assert_within(got, want, bound, what)
+        # a plain bf16 copy is not as good
+        assert float(((want.to(torch.bfloat16).double() - want).abs() > bound).double().mean()) > 0.2
+
+
+@pytest.mark.parametrize("act,dead", [("silu", -20.0), ("gelu", -5.5)])
+def test_saved_tensors_keep_small_values_beside_large_ones(cuda_ok, act, dead):
+    # a feature whose gate is shut, among features whose gates are wide open: its gradients keep bf16's
+    # 8 bits (one rounding of the kept value, one of du or dg)
+    f, d, rows = 64, 8, 1
+    z = torch.full((f,), 200.0)
+    z[::8] = dead
+    zu = torch.full((f,), 1024.0)
+    zu[3::8] = 0.0
+    one = lambda *s: torch.ones(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    zero = torch.zeros(1, f, d, dtype=torch.bfloat16, device="cuda")
+    w_down = torch.zeros(1, d, f, dtype=torch.bfloat16, device="cuda")
+    w_down[0, 0] = 1.0
+    args = moe.gated_ffn_args(one(rows, d), torch.tensor([0, rows], dtype=torch.int32, device="cuda"), zero,
+                              zero, w_down, b_gate=z.to(torch.bfloat16)[None].cuda(),
+                              b_up=zu.to(torch.bfloat16)[None].cuda(), act=act)
+    r = moe.moe_gated_ffn(args, train=True)
+    g = moe.moe_gated_ffn_backward(args, one(rows, d), r["h_packed"], r["saved"])
+    a, _, da, _ = exact(z, act)
+    for name, want in (("dw_up", a), ("dw_gate", zu.double() * da)):
+        got = g[name][0].double().cpu()
+        for j in range(d):
+            assert_within(got[:, j], want, (2 * 2.0 ** -8 + 2.0 ** -14) * want.abs() + 1e-300, name)
+
+
 def test_fp32_nan_of_any_payload(cuda_ok):
     # NaNs whose payload lies in the low bits only: the two-part split may not turn them into infinities
     # (second parts of the weights have the first ones' sign, so infinities would not cancel)
