@@ -37,7 +37,9 @@
  *   - bf16 tensors are stored as 16-bit words (the top half of an IEEE fp32 word).
  *   - Environment variable MOE_FAULT_INJECT=<entry point name> makes that entry point
  *     return MOE_ERR_CUDA without enqueueing anything (host-side fault injection for
- *     callers' error paths).
+ *     callers' error paths). MOE_FAULT_INJECT=clusters, set before the first call, makes the
+ *     gated products run as where the device holds no thread-block clusters (all but the weight
+ *     gradients of bf16 layers, which need pairs).
  *   - Performance switches, all on by default and all bit-identical in their results
  *     (set to 0 to turn one off, for A/B timing): MOE_PDL (programmatic dependent launch
  *     between the layer's kernels; read once per process), MOE_FUSED_ROUTER (softmax,

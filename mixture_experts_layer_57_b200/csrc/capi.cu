@@ -62,6 +62,47 @@ int num_sms() {
   return n;
 }
 
+bool fault_injected(const char* entry) {
+  const char* v = std::getenv("MOE_FAULT_INJECT");
+  return v != nullptr && std::strcmp(v, entry) == 0;
+}
+
+cudaError_t cluster_slots(const void* kern, int width, int threads, int smem,
+                          std::atomic<int>* cache, int* slots) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  const int known = cache[dev].load(std::memory_order_relaxed);
+  if (known != 0) {
+    *slots = known - 1;
+    return cudaSuccess;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)width);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)width;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  *slots = 0;
+  if (width == 1 || !fault_injected("clusters")) {
+    e = cudaOccupancyMaxActiveClusters(slots, kern, &cfg);
+    if (e == cudaErrorInvalidClusterSize) {  // as good as none
+      cudaGetLastError();
+      *slots = 0;
+    } else if (e != cudaSuccess) {
+      return e;
+    }
+  }
+  cache[dev].store(*slots + 1, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -73,11 +114,6 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-bool fault_injected(const char* entry) {
-  const char* v = std::getenv("MOE_FAULT_INJECT");
-  return v != nullptr && std::strcmp(v, entry) == 0;
-}
 
 size_t esize(moe_dtype dt) { return dt == MOE_BF16 ? 2 : 4; }
 

@@ -755,35 +755,15 @@ cudaError_t launch_clusters(const Config& c, int64_t tiles, cudaStream_t stream,
 }
 
 // The kernel for a mode in clusters of `width`, with its slots on this device (asked once per
-// kernel, width and device).
+// kernel, width and device; 0: such clusters do not fit).
 template <int OP, int BN, int FT, int MODE>
 cudaError_t config_of(int width, Config* c) {
   *c = Config{gated_gemm_kernel<OP, BN, FT, MODE>, GemmCfg<OP, BN, FT, MODE>::kSmemBytes, width, 0};
   static int attr_done[64] = {0};  // per instantiation and device
   cudaError_t e = ensure_dynamic_smem(c->kern, c->smem, attr_done);
   if (e != cudaSuccess) return e;
-  static std::atomic<int> slots[64][kMaxSplit + 1];
-  int dev = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  std::atomic<int>& cached = slots[dev][width];
-  if ((c->slots = cached.load(std::memory_order_relaxed)) == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)width);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = c->smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)width;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if ((e = cudaOccupancyMaxActiveClusters(&c->slots, c->kern, &cfg)) != cudaSuccess) return e;
-    if (c->slots < 1) return cudaErrorLaunchOutOfResources;
-    cached.store(c->slots, std::memory_order_relaxed);
-  }
-  return cudaSuccess;
+  static std::atomic<int> cache[kMaxSplit + 1][kMaxDevices];
+  return cluster_slots((const void*)c->kern, width, kThreads, c->smem, cache[width], &c->slots);
 }
 
 template <int OP, int BN>
@@ -832,6 +812,7 @@ cudaError_t launch_op(const GemmMaps& m, const GemmParams& p, int64_t capacity_h
     Config c{};
     const cudaError_t e = config_of<OP>(bn, ft, mode, width, &c);
     if (e != cudaSuccess) return e;
+    if (c.slots < 1) return cudaSuccess;  // not on this device
     const int feats = feat * ft * (mode == kPair ? 2 : 1);
     const int64_t tiles = experts * ((rows + bn - 1) / bn) * ((p.n_out + feats - 1) / feats);
     const int64_t rounds = (tiles + c.slots - 1) / c.slots;
@@ -857,7 +838,9 @@ cudaError_t launch_op(const GemmMaps& m, const GemmParams& p, int64_t capacity_h
   for (int width = 1; width <= kMaxSplit && n_blocks >= 4 * width; ++width)
     if (e == cudaSuccess && parts_of(std::min(fit, 128), width) <= kPartChunks)
       e = consider(std::min(fit, 128), 1, kSplit, width);
+  if (e == cudaSuccess && best.kern == nullptr) e = consider(std::min(fit, 128), 1, kSplit, 1);
   if (e != cudaSuccess) return e;
+  if (best.kern == nullptr) return cudaErrorLaunchOutOfResources;
   return launch_clusters(best, best_tiles, stream, m, p);
 }
 

@@ -23,6 +23,7 @@
 // bounds it: the loads and splits, some 2000 cycles for 32 of K and 128 rows (three tf32 MMA passes:
 // 768). 4 experts, 1000 rows, d 501, f 1334: up 67 us, down 60 (tiles of fp32 FMAs: 123 and 115).
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "gated.cuh"
@@ -598,20 +599,28 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tf32_kernel(const Args p) {
   }
 }
 
-// Clusters of `split` CTAs, one CTA to an SM, that run at once: a few of those of four that the SMs
-// would make do not fit the device's groups of SMs (33 of 37).
-int64_t clusters_at_once(int split) {
-  return split == 1 ? num_sms() : std::max(1, num_sms() / split - 4);
+// Tiles of a kernel that run at once: one CTA to an SM, or as many clusters as the device holds (33 of
+// four where 148 SMs would make 37); 0: such clusters do not fit.
+template <int OP, bool WIDE, int BN, int SPLIT>
+cudaError_t tiles_at_once(int* n) {
+  auto kern = gated_tf32_kernel<OP, WIDE, BN, SPLIT>;
+  constexpr int smem = Cfg<BN, SPLIT>::kSmemBytes;
+  static int attr_done[64] = {0};  // per instantiation and device
+  const cudaError_t e = ensure_dynamic_smem(kern, smem, attr_done);
+  *n = num_sms();
+  if (SPLIT == 1 || e != cudaSuccess) return e;
+  static std::atomic<int> cache[kMaxDevices];
+  return cluster_slots((const void*)kern, SPLIT, kThreads, smem, cache, n);
 }
 
 template <int OP, bool WIDE, int BN, int SPLIT>
 cudaError_t launch_as(const Args& p, int64_t tiles, cudaStream_t stream) {
   auto kern = gated_tf32_kernel<OP, WIDE, BN, SPLIT>;
   constexpr int smem = Cfg<BN, SPLIT>::kSmemBytes;
-  static int attr_done[64] = {0};  // per instantiation and device
-  const cudaError_t e = ensure_dynamic_smem(kern, smem, attr_done);
+  int at_once = 0;
+  const cudaError_t e = tiles_at_once<OP, WIDE, BN, SPLIT>(&at_once);
   if (e != cudaSuccess) return e;
-  const unsigned clusters = (unsigned)std::min<int64_t>(tiles, clusters_at_once(SPLIT));
+  const unsigned clusters = (unsigned)std::min<int64_t>(tiles, at_once);
   if constexpr (SPLIT == 1) return launch_kernel(kern, dim3(clusters), dim3(kThreads), smem, stream, p);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(clusters * SPLIT);
@@ -645,9 +654,12 @@ cudaError_t launch_walk(const Args& p, int64_t capacity_hint, cudaStream_t strea
     return std::min<int64_t>(p.E, p.rows_max) * over(rows, bn) * over(p.n_out, OP == kUp ? kBM / 2 : kBM);
   };
   const int64_t blocks = (OP == kInput ? 2 : 1) * over(OP == kWeight ? rows : p.K, kBK);
-  const double t128 = (double)over(tiles(128), clusters_at_once(1)) * blocks;
-  const double t64 = over(tiles(64), clusters_at_once(1)) * 0.65 * blocks;
-  const double t64x4 = over(tiles(64), clusters_at_once(4)) * (0.65 * over(blocks, 4) + 3);
+  int fours = 0;
+  const cudaError_t e = tiles_at_once<OP, WIDE, 64, 4>(&fours);
+  if (e != cudaSuccess) return e;
+  const double t128 = (double)over(tiles(128), num_sms()) * blocks;
+  const double t64 = over(tiles(64), num_sms()) * 0.65 * blocks;
+  const double t64x4 = fours < 1 ? t128 : over(tiles(64), fours) * (0.65 * over(blocks, 4) + 3);
   if (t64x4 < t128 && t64x4 < t64) return launch_as<OP, WIDE, 64, 4>(p, tiles(64), stream);
   if (t64 < t128) return launch_as<OP, WIDE, 64, 1>(p, tiles(64), stream);
   return launch_as<OP, WIDE, 128, 1>(p, tiles(128), stream);

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/moe.h"
 
 namespace moe {
@@ -15,6 +17,16 @@ void reset_launch_count();
 
 // Number of SMs of the current device (cached per device).
 int num_sms();
+
+// Whether MOE_FAULT_INJECT names this entry point (or, "clusters", what cluster_slots answers).
+bool fault_injected(const char* entry);
+
+// Clusters of `width` CTAs of a kernel that the current device holds at once, 0 if not one (a context
+// with few SMs; MOE_FAULT_INJECT=clusters: any of several CTAs). cache: kMaxDevices entries, zero at
+// first, of this kernel and width. The kernel's dynamic shared memory has been allowed before.
+constexpr int kMaxDevices = 64;
+cudaError_t cluster_slots(const void* kern, int width, int threads, int smem,
+                          std::atomic<int>* cache, int* slots);
 
 // Whether launches carry the programmatic-dependent-launch attribute (MOE_PDL=0 disables it).
 bool pdl_enabled();
