@@ -426,7 +426,8 @@ moe_status moe_layer_backward(const moe_layer_args* args, const void* d_out, flo
  * not non-decreasing within [0, rows_max] set MOE_DEVERR_BAD_OFFSETS. capacity_hint: an upper bound on the rows of
  * any one expert (normally C); it selects tile sizes and how sums are split, so it may change
  * results in their rounding, and is otherwise free to be wrong.
- * Limits: those of moe_expert_ffn (bf16: d_model and d_ff multiples of 8). Both types run on tcgen05
+ * Limits: those of moe_expert_ffn (bf16: d_model and d_ff multiples of 8), rows_max up to 2^30 and
+ * widths up to 2^29. Both types run on tcgen05
  * tensor cores and accumulate in fp32. fp32 factors are split in two tf32 parts each, which keeps
  * sums as exact as fp32 FMAs' (products within 2^-21) for factors from 2^-100 up to 2^127; smaller ones
  * keep fewer bits (11 at 2^-126), larger ones 20, and an infinite factor makes its sums NaN. fp32 calls of up to 8 rows without saved run on fp32 FMA. */

@@ -1364,9 +1364,15 @@ moe_status moe_layer_backward(const moe_layer_args* args, const void* d_out, flo
 
 namespace {
 
+// Sizes up to which the kernels' 32-bit row, column and tile arithmetic holds, sums of a tile's
+// extent with a size and of three widths included.
+constexpr int64_t kGatedMaxRows = (int64_t)1 << 30, kGatedMaxWidth = (int64_t)1 << 29;
+
 moe_status check_gated(const moe_gated_ffn_args* a) {
   const moe_status st = check_ffn_shape(a->E, a->rows_max, a->d_model, a->d_ff, a->dtype);
   if (st != MOE_OK) return st;
+  if (a->rows_max > kGatedMaxRows || a->d_model > kGatedMaxWidth || a->d_ff > kGatedMaxWidth)
+    return MOE_ERR_UNSUPPORTED;
   if (!valid_dtype(a->out_dtype) || (a->act != MOE_GATE_SILU && a->act != MOE_GATE_GELU))
     return MOE_ERR_INVALID_ARGUMENT;
   if (a->dtype == MOE_F32 && a->out_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;

@@ -120,7 +120,7 @@ struct Walk {
       mt = tf;
       nt = td;
     }
-    // v < 2^13 (d, f <= 16384): exact
+    // v < 2^24 in any gradients that fit in memory (256 x 256 elements to a tile, or widths up to 2^29)
     const unsigned band = kGroup * nt, g = div_small(v, band);
     v -= g * band;
     const unsigned high = min((unsigned)kGroup, mt - g * kGroup), n = div_small(v, high);
@@ -128,7 +128,7 @@ struct Walk {
     w.n0 = (int)n * kTile;
     return w;
   }
-  // v / by for v below 2^20: a float quotient, whose error is under one step, put right
+  // v / by: a float quotient, exact to 2^-22 of it, so off by one step at most below 2^22, put right
   static __device__ __forceinline__ unsigned div_small(unsigned v, unsigned by) {
     unsigned q = (unsigned)__fdividef((float)v, (float)by);
     if (q * by > v) --q;
