@@ -11,6 +11,8 @@
 //
 // Launch overlap: both kernels let their successor start at once, and a single expert's weights are
 // asked into L2 before the wait for what comes before.
+#include <type_traits>
+
 #include "common.cuh"
 #include "gated.cuh"
 #include "kernels.h"
@@ -19,6 +21,7 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kAhead = 8;  // K elements of a lane whose weights are loaded together
 
 struct GemvArgs {
   const int32_t* offsets;
@@ -39,7 +42,7 @@ __device__ __forceinline__ int segment_at(const GemvArgs& p, int& rows) {
   }
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += 32 * kWarps) {
-    const int a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
+    const int a = p.offsets[e], b = p.offsets[e + 1];
     if (a < 0 || b < a || (int64_t)b > p.rows_max) {
       bad = 1;
     } else if (a == (int)blockIdx.y && b > a) {
@@ -85,18 +88,35 @@ __global__ void __launch_bounds__(32 * kWarps) gated_gemv_kernel(const GemvArgs 
   float g[NR], u[NR];
 #pragma unroll
   for (int r = 0; r < NR; ++r) g[r] = u[r] = 0.0f;
-#pragma unroll 8
-  for (int k = lane; k < p.K; k += 32) {
-    const float a = __ldg(w0 + k), b = UP ? __ldg(w1 + k) : 0.0f;
+  // kAhead weights of each matrix are under way before the first is used; plain loads, as the rows may
+  // be written until the wait above is over
+  int k = lane;
+  auto part = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    float a[N], b[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      a[j] = w0[k + 32 * j];
+      b[j] = UP ? w1[k + 32 * j] : 0.0f;
+    }
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       if (r < rows) {
-        const float x = __ldg(in + (int64_t)r * p.K + k);
-        g[r] = fmaf(a, x, g[r]);
-        if constexpr (UP) u[r] = fmaf(b, x, u[r]);
+        const float* x = in + (int64_t)r * p.K + k;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const float v = x[32 * j];
+          g[r] = fmaf(a[j], v, g[r]);
+          if constexpr (UP) u[r] = fmaf(b[j], v, u[r]);
+        }
       }
     }
-  }
+    k += 32 * N;
+  };
+#pragma unroll 1
+  while (k + 32 * (kAhead - 1) < p.K) part(std::integral_constant<int, kAhead>());
+#pragma unroll 1
+  while (k < p.K) part(std::integral_constant<int, 1>());
   const int64_t bi = (int64_t)e * p.n_out + f;
   const float bg = p.b0 != nullptr ? p.b0[bi] : 0.0f, bu = UP && p.b1 != nullptr ? p.b1[bi] : 0.0f;
 #pragma unroll

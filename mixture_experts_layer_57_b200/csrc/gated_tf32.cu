@@ -108,7 +108,7 @@ __device__ __forceinline__ Tile tile_at(const Args& p, int t, const int* prefix,
     w.f0 = u / nt * kBM;
     w.row0 = u % nt * BN;
     w.n_valid = min(BN, rows - w.row0);
-    int a = __ldg(p.offsets + w.e), b = __ldg(p.offsets + w.e + 1);
+    int a = p.offsets[w.e], b = p.offsets[w.e + 1];
     if (a < 0 || b < a || (int64_t)b > p.rows_max) a = b = 0;  // flagged by the passes before
     w.seg = a;
     w.K = b - a;
@@ -201,16 +201,16 @@ __device__ __forceinline__ void load_block(float (&v)[R / 8], const float* at, i
     const float* from = W == kAcross ? at + k * ld : at + i * step + k;
     const bool mine = (ok >> i & 1u) != 0;
     if constexpr (W == kWide) {
-      const float4 q = mine && k < K ? __ldg(reinterpret_cast<const float4*>(from))  // K % 4 == 0
+      const float4 q = mine && k < K ? *reinterpret_cast<const float4*>(from)  // K % 4 == 0
                                      : make_float4(0.f, 0.f, 0.f, 0.f);
       v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
     } else if (k0 + kBK <= K) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[4 * i + j] = mine ? __ldg(from + (W == kAcross ? j * ld : j)) : 0.0f;
+      for (int j = 0; j < 4; ++j) v[4 * i + j] = mine ? from[W == kAcross ? j * ld : j] : 0.0f;
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        v[4 * i + j] = mine && k + j < K ? __ldg(from + (W == kAcross ? j * ld : j)) : 0.0f;
+        v[4 * i + j] = mine && k + j < K ? from[W == kAcross ? j * ld : j] : 0.0f;
     }
   }
 }

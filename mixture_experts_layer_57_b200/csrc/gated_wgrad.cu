@@ -91,7 +91,7 @@ struct Walk {
       ++e;
     }
     if (e < p.E) {
-      int a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
+      int a = p.offsets[e], b = p.offsets[e + 1];
       if (a < 0 || b < a || (int64_t)b > p.rows_max) a = b = 0;  // invalid: treated as empty
       row0 = a;
       rows = b - a;
