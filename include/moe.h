@@ -419,8 +419,8 @@ moe_status moe_layer_backward(const moe_layer_args* args, const void* d_out, flo
  * saved: NULL, or [2, rows_max, d_ff] in dtype for the backward pass, which alone reads it: plane 0
  * receives act(zg), plane 1 zu act'(zg) (bf16 layers: eight neighbours in 16 bits each with one
  * exponent between them: 11 bits of those within 2^-12 of the largest and at least bf16's 8 of every
- * other; where one of the eight lies below some 2^-16 of the largest, 8 bits of all, and beside a
- * magnitude of 2^126 or more, an infinity or a NaN, 7).
+ * other down to 2^-124 of it; where one of the eight lies below some 2^-16 of the largest, 8 bits of
+ * all, and beside a magnitude of 2^126 or more, an infinity or a NaN, the first 7).
  * Rows outside every segment are not written and their values do not matter (NaN included). No
  * output may overlap another tensor of the call; inputs may (w_up may be w_gate). Offsets that are
  * not non-decreasing within [0, rows_max] set MOE_DEVERR_BAD_OFFSETS. capacity_hint: an upper bound on the rows of

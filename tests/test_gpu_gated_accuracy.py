@@ -139,6 +139,28 @@ def test_saved_tensors_keep_small_values_beside_large_ones(cuda_ok, act, dead):
             assert_within(got[:, j], want, (2 * 2.0 ** -8 + 2.0 ** -14) * want.abs() + 1e-300, name)
 
 
+def test_saved_tensors_beside_a_magnitude_past_the_scale(cuda_ok):
+    # a value of 2^126 or more, or an infinity: its seven neighbours keep the sign, the exponent and six
+    # bits of mantissa of their own, cut (up to 2^-6 of the value)
+    gen = torch.Generator().manual_seed(2)
+    z = (2 * torch.randn(512, generator=gen)).to(torch.bfloat16).float()
+    zu = (torch.randn(512, generator=gen) * 2.0 ** 20).to(torch.bfloat16).float()
+    big = torch.arange(512) % 8 == 3
+    a, _, da, _ = exact(z, "silu")
+    for value in (3e38, 2.0 ** 126, float("inf")):
+        zu[big] = value
+        _, saved = block(z, zu, torch.bfloat16, "silu")
+        q, want = unpack(saved[1]), zu.double() * da
+        assert_within(q[~big], want[~big], (2.0 ** -6 + 2.0 ** -16) * want[~big].abs()
+                      + zu.double().abs()[~big] * 2.0 ** -18, "neighbours")
+        if value == float("inf"):
+            assert bool((q[big] == want[big]).all())
+        else:
+            near = want[big].abs() >= 2.0 ** 126
+            assert_within(q[big][near], want[big][near], 2.0 ** -5.9 * want[big][near].abs(), "large")
+        assert_within(unpack(saved[0]), a, 2.0 ** -7.9 * a.abs(), "act")
+
+
 def test_fp32_nan_of_any_payload(cuda_ok):
     # NaNs whose payload lies in the low bits only: the two-part split may not turn them into infinities
     # (second parts of the weights have the first ones' sign, so infinities would not cancel)
