@@ -430,7 +430,9 @@ moe_status moe_layer_backward(const moe_layer_args* args, const void* d_out, flo
  * widths up to 2^29. Both types run on tcgen05
  * tensor cores and accumulate in fp32. fp32 factors are split in two tf32 parts each, which keeps
  * sums as exact as fp32 FMAs' (products within 2^-21) for factors from 2^-100 up to 2^127; smaller ones
- * keep fewer bits (11 at 2^-126), larger ones 20, and an infinite factor makes its sums NaN. fp32 calls of up to 8 rows without saved run on fp32 FMA. */
+ * keep fewer bits (11 at 2^-126), larger ones 20, and an infinite factor makes its sums NaN. fp32 calls
+ * without saved of up to 8 rows run on fp32 FMA where capacity_hint leaves one expert 5 at most or
+ * d_model d_ff is at most 2^19. */
 typedef enum { MOE_GATE_SILU = 0, MOE_GATE_GELU = 1 } moe_gate_act;
 typedef struct {
   const void* x_packed;

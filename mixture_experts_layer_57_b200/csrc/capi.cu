@@ -1440,7 +1440,7 @@ moe_status moe_gated_ffn(const moe_gated_ffn_args* args, void* h_packed, void* y
   const GatedFfn g = gated_of(args);
   int* status = (int*)ws;
   cudaError_t e;
-  if (args->dtype == MOE_F32 && saved == nullptr && args->rows_max <= kGatedGemvRows) {
+  if (args->dtype == MOE_F32 && saved == nullptr && gated_gemv_f32_suits(g)) {
     e = enqueue_gated_gemv_f32(g, (float*)h_packed, (float*)y_packed, status, stream);
   } else if (args->dtype == MOE_BF16) {
     e = enqueue_gated_up_bf16(g, h_packed, saved, saved_q, status, stream);

@@ -2,15 +2,20 @@
 //     h[r, i] = act(Wg[e][i] . x[r] + bg) * (Wu[e][i] . x[r] + bu),   y[r, m] = Wd[e][m] . h[r] + bd
 //
 // Bound by the weights' stream: each is read once, for all rows of its expert, and used for as many
-// products as there are rows, which the FMA units keep up with. A warp computes one hidden feature
-// (a row of Wg and one of Wu) or one output (a row of Wd), its lanes side by side along the row, sums
-// in fp32 and then over the lanes: no tiles to fill, so every SM takes part. One row of a 700 x 2000
-// layer: 21 us, on the split-tf32 tiles 106; eight rows 49 and 109. bf16 layers stay on their tiles,
-// which stream as fast (one row of 2048 x 8192, weights cold: 43 us this way, 40 on the tiles; four
-// rows 69 and 40).
+// products as there are rows, which the FMA units keep up with for a few. A warp computes one hidden
+// feature (a row of Wg and one of Wu) or one output (a row of Wd), its lanes side by side along the row,
+// sums in fp32 and then over the lanes: no tiles to fill, so every SM takes part. Against the split-tf32
+// tiles (us a call, weights that fit in L2 resident): 700 x 2000 of one expert, 1 row 14 and 32, 4 rows
+// 27 and 33, 5 rows 27 and 33, 8 rows 38 and 33; 2048 x 8192, 1 row 66 and 149 (3.0 TB/s), 3 rows 148
+// and 149, 5 rows 161 and 150, 8 rows 250 and 150; 8 rows of 512 x 1024 22 and 25; 8 rows over 8 experts
+// of 1024 x 4096, 75 and 221. So experts with more than five rows go to the tiles unless the layer is
+// small (gated_gemv_f32_suits). bf16 layers stay on their tiles, which stream as fast
+// (when this form was tried there, one row of 2048 x 8192, weights cold: 43 us this way, 40 on the
+// tiles; four rows 69 and 40).
 //
 // Launch overlap: both kernels let their successor start at once, and a single expert's weights are
 // asked into L2 before the wait for what comes before.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.cuh"
@@ -144,6 +149,12 @@ cudaError_t launch(const GemvArgs& p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+bool gated_gemv_f32_suits(const GatedFfn& g) {
+  constexpr int64_t kExpertRows = 5, kSmall = 1 << 19;  // the figures at the top
+  return g.rows_max <= kGatedGemvRows &&
+         (std::min(g.capacity_hint, g.rows_max) <= kExpertRows || (int64_t)g.d * g.f <= kSmall);
+}
 
 cudaError_t enqueue_gated_gemv_f32(const GatedFfn& g, float* h, float* y, int* status,
                                    cudaStream_t stream) {

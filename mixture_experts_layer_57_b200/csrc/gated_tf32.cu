@@ -20,8 +20,9 @@
 // K-major in the swizzled layout of the MMA. The lanes of the accumulator are the output's
 // contiguous index, so stores go out as whole lines. Tiles are of 128 features and 128 or 64 rows, or
 // 64 rows with K over clusters of four CTAs that exchange their sums (launch_walk chooses). What
-// bounds it: the loads and splits, some 2000 cycles for 32 of K and 128 rows (three tf32 MMA passes:
-// 768). 4 experts, 1000 rows, d 501, f 1334: up 67 us, down 60 (tiles of fp32 FMAs: 123 and 115).
+// bounds it: the loads and splits, some 4000 cycles for 32 of K and 128 rows, 2800 for 64 rows, of which
+// the tensor pipe is at work for 850; 30% of the issue slots are taken (148 tiles of 128 rows, K 2048).
+// 4 experts, 1000 rows, d 501, f 1334: up 61 us, down 52 (tiles of fp32 FMAs: 123 and 115).
 #include <algorithm>
 #include <atomic>
 
@@ -218,7 +219,8 @@ __device__ __forceinline__ void load_block(float (&v)[R / 8], const float* at, i
 // hi: x rounded to 11 bits (tf32), lo: the exact rest, rounded to 11. Where one of the four is 2^127
 // or more, infinite or NaN, both are cut instead: hi does not overflow, and of a NaN, whose payload may
 // be cut from hi, x - hi is a NaN that lo keeps (rounding up would carry it into -0). x - hi is NaN for
-// an infinite x too, so its sums are NaN. (A NaN made quiet in hi: 132 us for 108, 1000 rows below.)
+// an infinite x too, so its sums are NaN. (A NaN made quiet in hi instead: the forward pass of 1000
+// rows, d 501, f 1334, takes 132 us for 108.)
 __device__ __forceinline__ void split4(const float* x, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
   float m = fabsf(x[0]);
 #pragma unroll

@@ -404,8 +404,10 @@ cudaError_t enqueue_gated_weight_grad_bf16(const GatedFfn& g, const void* dy, co
                                            const void* dg, const void* du, void* dw_down,
                                            void* dw_gate, void* dw_up, bool grad_bf16, int* status,
                                            cudaStream_t stream);
-// The forward pass of up to kGatedGemvRows fp32 rows, both launches, without the saved tensors.
+// The forward pass of up to kGatedGemvRows fp32 rows, both launches, without the saved tensors, and
+// whether it is faster than the tiles.
 constexpr int kGatedGemvRows = 8;
+bool gated_gemv_f32_suits(const GatedFfn& g);
 cudaError_t enqueue_gated_gemv_f32(const GatedFfn& g, float* h, float* y, int* status,
                                    cudaStream_t stream);
 // Bias gradients: column sums of up to three matrices over each segment's rows, in one launch
