@@ -127,9 +127,9 @@ __device__ __forceinline__ void unpack_block8(const uint4& q, float (&v)[8]) {
   }
 }
 
-// Tiled bulk tensor copies global -> shared of three and four dimensions, completion counted on
-// `bar` in bytes; the _pair forms land in this CTA and count on an mbarrier of either CTA of a
-// pair (a shared::cluster address).
+// Tiled bulk tensor copies global -> shared of three dimensions, completion counted on `bar` in bytes;
+// the _pair form lands in this CTA and counts on an mbarrier of either CTA of a pair (a shared::cluster
+// address).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int32_t x, int32_t y,
                                             int32_t z, uint32_t bar) {
   asm volatile(
@@ -138,29 +138,12 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int3
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int32_t x, int32_t y,
-                                            int32_t z, int32_t w, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
-}
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap, int32_t x,
                                                  int32_t y, int32_t z, uint32_t cluster_bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void* tmap, int32_t x,
-                                                 int32_t y, int32_t z, int32_t w,
-                                                 uint32_t cluster_bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(cluster_bar)
       : "memory");
 }
 

@@ -12,7 +12,9 @@
 //
 // Up projection: both weights meet in one accumulator. The 128 rows of an A tile are eight groups
 // of 16: gate features f0..f0+15, up features f0..f0+15, gate f0+16.., and so on, each group one
-// TMA box. A warp's 32 TMEM lanes then hold zg and zu of the same 16 features, half a warp apart;
+// TMA box of its own tensor. (One tensor map over both, with their distance as a stride, is not sound:
+// the memory between two allocations need not be mapped, and with the first tensor near the end of its
+// allocation such loads ended in an illegal access, although every box lay inside the two tensors.) A warp's 32 TMEM lanes then hold zg and zu of the same 16 features, half a warp apart;
 // eight shuffles per 16 tokens give every lane zg and zu of one feature for eight tokens, so the
 // activation and the product cost no extra pass, no extra accumulator and no shared memory.
 //
@@ -57,8 +59,6 @@ struct GemmParams {
   int out_bf16;              // kDown, kInput
   int act;
   int* status;
-  int joint;    // kUp: one box of a four-dimensional map brings gate and up rows together
-  int up_first; // kUp: in that map the up projection's rows come first
 };
 
 // A and B of each product; the token operand with both box heights.
@@ -221,12 +221,6 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* m, int 
   if constexpr (MODE == kPair) tma_load_3d_pair(dst, m, x, y, z, bar);
   else tma_load_3d(dst, m, x, y, z, bar);
 }
-template <int MODE>
-__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* m, int x, int y, int z,
-                                        int w, uint32_t bar) {
-  if constexpr (MODE == kPair) tma_load_4d_pair(dst, m, x, y, z, w, bar);
-  else tma_load_4d(dst, m, x, y, z, w, bar);
-}
 
 // Loads the A tile(s) of one stage: feature f0 of expert e on, K block kb of product `ph`.
 template <int OP, int FT, int MODE>
@@ -239,14 +233,10 @@ __device__ __forceinline__ void load_a(uint32_t sa, const GemmMaps& m, const Gem
       // rows past this expert's features belong to the next expert or are out of range; the
       // epilogue masks them
       const int w_row = e * p.n_out + f0 + i * (kBM / 2);
-      if (p.joint) {
-        load_4d<MODE>(sai, &m.a0, kb * kBK, 0, 0, w_row >> 4, bar);
-      } else {
 #pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
-          load_2d<MODE>(sai + g * 4096, &m.a0, kb * kBK, w_row + g * 16, bar);
-          load_2d<MODE>(sai + g * 4096 + 2048, &m.a1, kb * kBK, w_row + g * 16, bar);
-        }
+      for (int g = 0; g < 4; ++g) {
+        load_2d<MODE>(sai + g * 4096, &m.a0, kb * kBK, w_row + g * 16, bar);
+        load_2d<MODE>(sai + g * 4096 + 2048, &m.a1, kb * kBK, w_row + g * 16, bar);
       }
     } else if constexpr (OP == kDown) {
       load_2d<MODE>(sai, &m.a0, kb * kBK, e * p.n_out + f0 + i * kBM, bar);
@@ -307,7 +297,7 @@ __device__ __forceinline__ void load_hidden_in(HiddenIn& in, const GemmParams& p
 // warp apart.
 __device__ __forceinline__ void finish_up(const Tile& tl, const GemmParams& p, const uint32_t (&r)[16],
                                           int fw, int c0, float bg, float bu, int lane, uint8_t* st) {
-  const int j = lane & 15, hi = lane >> 4, up = hi ^ p.up_first;
+  const int j = lane & 15, hi = lane >> 4;
   uint16_t* s16 = reinterpret_cast<uint16_t*>(st);       // h: [16 tokens][16 features]
   float* s32 = reinterpret_cast<float*>(st + 512);       // a, then q: the same, 16 floats between
                                                          // tokens 7 and 8 (bank conflicts)
@@ -318,8 +308,8 @@ __device__ __forceinline__ void finish_up(const Tile& tl, const GemmParams& p, c
     // the lower lanes keep tokens 0..7 and give 8..15, the upper ones the other way round
     const float own = __uint_as_float(hi ? r[8 + i] : r[i]);
     const float got = __shfl_xor_sync(0xffffffffu, __uint_as_float(hi ? r[i] : r[8 + i]), 16);
-    const float zg = (up ? got : own) + bg;
-    const float zu = (up ? own : got) + bu;
+    const float zg = (hi ? got : own) + bg;
+    const float zu = (hi ? own : got) + bu;
     float da;
     gate_act<true>(zg, p.act, a[i], da);
     q[i] = zu * da;
@@ -710,22 +700,6 @@ bool weight_map_mn(CUtensorMap* m, const void* ptr, int E, int K, int n) {
   return encode_map(m, ptr, 3, extent, stride, box);
 }
 
-// Both projections' rows [E * f, d] as one tensor [groups of 16 rows][2 projections][16 rows][d],
-// whose box of four groups is a whole A tile: the projections lie a fixed distance apart, which is
-// the stride of the second dimension from outside. Experts must start on a group (f % 16 == 0) and
-// the distance fit a stride (below 2^40); otherwise false, and 16-row boxes do.
-bool joint_map(CUtensorMap* m, const GatedFfn& g, int* up_first) {
-  const uintptr_t wg = (uintptr_t)g.w_gate, wu = (uintptr_t)g.w_up;
-  const uintptr_t lo = wg < wu ? wg : wu, apart = (wg < wu ? wu : wg) - lo;
-  if (g.f % 16 != 0 || apart == 0 || apart % 16 != 0 || apart >= ((uintptr_t)1 << 40)) return false;
-  *up_first = wu < wg ? 1 : 0;
-  const cuuint64_t row = (cuuint64_t)g.d * 2;
-  const cuuint64_t extent[4] = {(cuuint64_t)g.d, 16, 2, (cuuint64_t)g.E * g.f / 16};
-  const cuuint64_t stride[3] = {row, (cuuint64_t)apart, 16 * row};
-  const cuuint32_t box[4] = {kBK, 16, 2, 4};
-  return encode_map(m, (const void*)lo, 4, extent, stride, box);
-}
-
 // One way of running a product: the kernel, its clusters (CTAs of each, and how many of them the
 // device holds at once) and its shared memory.
 struct Config {
@@ -880,10 +854,8 @@ cudaError_t enqueue_gated_up_bf16(const GatedFfn& g, void* h, void* saved_a, voi
   if (g.rows_max == 0) return cudaSuccess;
   GemmMaps m;
   GemmParams p{};
-  p.joint = joint_map(&m.a0, g, &p.up_first) ? 1 : 0;
-  if (p.joint) m.a1 = m.a0;
-  else if (!make_bf16_map_2d(&m.a0, g.w_gate, (int64_t)g.E * g.f, g.d, kBK, 16) ||
-           !make_bf16_map_2d(&m.a1, g.w_up, (int64_t)g.E * g.f, g.d, kBK, 16))
+  if (!make_bf16_map_2d(&m.a0, g.w_gate, (int64_t)g.E * g.f, g.d, kBK, 16) ||
+      !make_bf16_map_2d(&m.a1, g.w_up, (int64_t)g.E * g.f, g.d, kBK, 16))
     return cudaErrorInvalidValue;
   if (!token_maps(&m.b0l, &m.b0s, g.x, g.rows_max, g.d)) return cudaErrorInvalidValue;
   m.b1l = m.b0l;

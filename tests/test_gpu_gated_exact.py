@@ -135,3 +135,25 @@ def test_long_segment(cuda_ok, dtype, rows):
         assert not torch.equal(t, torch.zeros_like(t)) and torch.equal(t, want["d" + k])
     less = expect(c, 1, slice(3, 3 + rows - 16))
     assert all(not torch.equal(less["d" + k], want["d" + k]) for k in PARAMS)
+
+
+@pytest.mark.parametrize("d,f", [(64, 272), (8, 608), (128, 48), (520, 1040)])
+@pytest.mark.parametrize("between", ["none", "rows of a group", "one row", "ends of allocations"])
+@pytest.mark.parametrize("order", [("w_gate", "w_up"), ("w_up", "w_gate")], ids=str)
+def test_places_of_the_projections(cuda_ok, d, f, between, order):
+    # the two weights side by side, at distances on and off whole groups of 16 rows, and each at the end of
+    # an allocation of its own, behind which memory need not be mapped
+    c = make([5, 0, 70, 33], d, f, torch.bfloat16, seed=d + f)
+    n = 4 * f * d
+    if between == "ends of allocations":
+        torch.cuda.empty_cache()
+        keep = [torch.empty(12 << 20, dtype=torch.bfloat16, device="cuda") for _ in order]
+        w = {k: s[-n:].view(4, f, d) for k, s in zip(order, keep)}
+    else:
+        gap = {"none": 0, "rows of a group": 16 * d, "one row": d}[between]
+        space = torch.full((2 * n + gap,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        w = {order[0]: space[:n].view(4, f, d), order[1]: space[n + gap:].view(4, f, d)}
+    for k in order:
+        w[k].copy_(c[k])
+    e = dict(c, **w)
+    check(e, run(e, "silu", torch.float32, torch.bfloat16))
