@@ -10,13 +10,16 @@
 // operand (N = the tile's rows, so a segment of few rows costs no padding): the accumulator holds
 // features in TMEM lanes and tokens in columns.
 //
-// Up projection: both weights meet in one accumulator. The 128 rows of an A tile are eight groups
-// of 16: gate features f0..f0+15, up features f0..f0+15, gate f0+16.., and so on, each group one
-// TMA box of its own tensor. (One tensor map over both, with their distance as a stride, is not sound:
-// the memory between two allocations need not be mapped, and with the first tensor near the end of its
-// allocation such loads ended in an illegal access, although every box lay inside the two tensors.) A warp's 32 TMEM lanes then hold zg and zu of the same 16 features, half a warp apart;
-// eight shuffles per 16 tokens give every lane zg and zu of one feature for eight tokens, so the
-// activation and the product cost no extra pass, no extra accumulator and no shared memory.
+// Up projection: both weights meet in one accumulator. Of the 128 rows of an A tile 64 are gate
+// features and 64 up features, each a TMA box of its own tensor, so zg of a feature lies in one warp's
+// TMEM lanes and zu in those of the warp two quarters on. The two exchange halves of every 16 tokens
+// through shared memory (a kilobyte each way, handed over by mbarriers) and then both have zg and zu of
+// 32 features for eight tokens: activation and product cost no extra pass and no extra accumulator.
+// (Groups of 16 rows of each, which need no exchange but shuffles in the warp, are boxes of 2 KB: decode
+// over 128 experts 647 us for 470. One tensor map over both weights, with their distance as a stride, is
+// not sound: the memory between two allocations need not be mapped, and with the first tensor near the
+// end of its allocation such loads ended in an illegal access, although every box lay inside the two
+// tensors.)
 //
 // Hidden: the epilogue reads a and q, and loads them for its next 16 tokens while it works on these.
 //
@@ -105,7 +108,7 @@ struct GemmCfg {
   static constexpr int kSmemBytes =
       1024 + kStages * kStageBytes + kPartBytes + kEpiWarps * kEpiTileBytes + kAuxBytes;
   static_assert(kStageBytes % 1024 == 0, "stage tiles must stay 1024-byte aligned");
-  static_assert(kStages >= 3 && 2 * kStages + 7 <= 64, "stages");
+  static_assert(kStages >= 3 && 2 * kStages + 7 + 2 * kEpiWarps <= 64, "stages, barriers");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
@@ -144,7 +147,8 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, int* s
 
 // The mbarriers of one CTA: S stage-full, S stage-empty, 2 accumulator-full, 2 accumulator-empty,
 // one drain barrier, and kSplit's two: the others' partial sums are written, and they have read
-// this CTA's. 8 bytes each from `base`.
+// this CTA's; kUp: two for every epilogue warp, its half of the exchange is written, and the other warp
+// has read it. 8 bytes each from `base`.
 struct Bars {
   uint32_t base;
   int S;
@@ -155,6 +159,8 @@ struct Bars {
   __device__ __forceinline__ uint32_t drain() const { return base + 8u * (2 * S + 4); }
   __device__ __forceinline__ uint32_t part_full() const { return base + 8u * (2 * S + 5); }
   __device__ __forceinline__ uint32_t part_free() const { return base + 8u * (2 * S + 6); }
+  __device__ __forceinline__ uint32_t given(int w) const { return base + 8u * (2 * S + 7 + 2 * w); }
+  __device__ __forceinline__ uint32_t taken(int w) const { return base + 8u * (2 * S + 8 + 2 * w); }
 };
 
 // Position in the stage ring.
@@ -233,11 +239,8 @@ __device__ __forceinline__ void load_a(uint32_t sa, const GemmMaps& m, const Gem
       // rows past this expert's features belong to the next expert or are out of range; the
       // epilogue masks them
       const int w_row = e * p.n_out + f0 + i * (kBM / 2);
-#pragma unroll 1
-      for (int g = 0; g < 4; ++g) {
-        load_2d<MODE>(sai + g * 4096, &m.a0, kb * kBK, w_row + g * 16, bar);
-        load_2d<MODE>(sai + g * 4096 + 2048, &m.a1, kb * kBK, w_row + g * 16, bar);
-      }
+      load_2d<MODE>(sai, &m.a0, kb * kBK, w_row, bar);
+      load_2d<MODE>(sai + kBM * kBK, &m.a1, kb * kBK, w_row, bar);
     } else if constexpr (OP == kDown) {
       load_2d<MODE>(sai, &m.a0, kb * kBK, e * p.n_out + f0 + i * kBM, bar);
     } else {
@@ -293,23 +296,45 @@ __device__ __forceinline__ void load_hidden_in(HiddenIn& in, const GemmParams& p
   }
 }
 
-// Up projection: 16 tokens of this warp's 16 features; zg and zu of a feature lie in lanes half a
-// warp apart.
-__device__ __forceinline__ void finish_up(const Tile& tl, const GemmParams& p, const uint32_t (&r)[16],
-                                          int fw, int c0, float bg, float bu, int lane, uint8_t* st) {
-  const int j = lane & 15, hi = lane >> 4;
-  uint16_t* s16 = reinterpret_cast<uint16_t*>(st);       // h: [16 tokens][16 features]
-  float* s32 = reinterpret_cast<float*>(st + 512);       // a, then q: the same, 16 floats between
-                                                         // tokens 7 and 8 (bank conflicts)
+// The exchange of the up projection: this epilogue warp, the one that holds the other projection's
+// pre-activations of the same 32 features, their staging tiles, and the phase of their barriers.
+struct Exchange {
+  Bars bars;
+  int self, other;
+  const float* theirs;
+  uint32_t phase;
+  bool up;  // this warp's accumulator lanes are up features
+  volatile int* abort;
+  int* status;
+};
+
+// Up projection: 16 tokens of this warp's 32 features of one projection. The warp of the gate features
+// gives tokens 8..15 and finishes 0..7, the other one the other way round. False: a wait expired.
+__device__ __forceinline__ bool finish_up(const Tile& tl, const GemmParams& p, const uint32_t (&r)[16],
+                                          int fw, int c0, float bg, float bu, int lane, uint8_t* st,
+                                          Exchange& x) {
+  float* give = reinterpret_cast<float*>(st);            // [8 tokens][32 features]
+  uint16_t* s16 = reinterpret_cast<uint16_t*>(st + 1024);  // h: the same
+  float* s32 = reinterpret_cast<float*>(st + 1024);        // a, then q: the same
+  if (!mbar_wait_warp(x.bars.taken(x.self), x.phase ^ 1u, x.abort, x.status)) return false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) give[i * 32 + lane] = __uint_as_float(x.up ? r[i] : r[8 + i]);
+  __syncwarp();
+  if (lane == 0) mbar_arrive(x.bars.given(x.self));
+  if (!mbar_wait_warp(x.bars.given(x.other), x.phase, x.abort, x.status)) return false;
+  float got[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) got[i] = x.theirs[i * 32 + lane];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(x.bars.taken(x.other));
+  x.phase ^= 1u;
   const bool save = p.out1 != nullptr;
   float a[8], q[8], h[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    // the lower lanes keep tokens 0..7 and give 8..15, the upper ones the other way round
-    const float own = __uint_as_float(hi ? r[8 + i] : r[i]);
-    const float got = __shfl_xor_sync(0xffffffffu, __uint_as_float(hi ? r[i] : r[8 + i]), 16);
-    const float zg = (hi ? got : own) + bg;
-    const float zu = (hi ? own : got) + bu;
+    const float own = __uint_as_float(x.up ? r[8 + i] : r[i]);
+    const float zg = (x.up ? got[i] : own) + bg;
+    const float zu = (x.up ? own : got[i]) + bu;
     float da;
     gate_act<true>(zg, p.act, a[i], da);
     q[i] = zu * da;
@@ -318,36 +343,40 @@ __device__ __forceinline__ void finish_up(const Tile& tl, const GemmParams& p, c
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
     const uint32_t two = pack_bf16x2(h[i], h[i + 1]);
-    s16[(hi * 8 + i) * 16 + j] = (uint16_t)two;
-    s16[(hi * 8 + i + 1) * 16 + j] = (uint16_t)(two >> 16);
+    s16[i * 32 + lane] = (uint16_t)two;
+    s16[(i + 1) * 32 + lane] = (uint16_t)(two >> 16);
   }
-  const int row = lane >> 1, ff = fw + 8 * (lane & 1);
-  const bool mine = c0 + row < tl.n_valid && ff < p.n_out;
-  const int64_t o = (int64_t)(tl.row0 + c0 + row) * p.n_out + ff;
+  __syncwarp();
+  // eight features of one token per lane
+  const int token = lane >> 2, row = c0 + (x.up ? 8 : 0) + token, ff = fw + 8 * (lane & 3);
+  const bool mine = row < tl.n_valid && ff < p.n_out;
+  const int64_t o = (int64_t)(tl.row0 + row) * p.n_out + ff;
+  if (mine)
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out0) + o) =
+        reinterpret_cast<const uint4*>(s16)[lane];
+  __syncwarp();
   if (save) {
-    float* put = s32 + (hi * 8) * 16 + hi * 16 + j;
-    const float4* get = reinterpret_cast<const float4*>(s32 + lane * 8 + hi * 16);
+    // the 16-byte halves in an order that spreads two tokens over all banks
+    const float4* get = reinterpret_cast<const float4*>(s32) + 2 * lane;
+    const int odd = token & 1;
     auto store = [&](void* out) {
-      const float4 x = get[0], y = get[1];
-      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      const float4 u = get[odd], w = get[odd ^ 1];
+      const float4 lo = odd ? w : u, hi = odd ? u : w;
+      const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
       if (mine) *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(out) + o) = pack_block8(v);
     };
 #pragma unroll
-    for (int i = 0; i < 8; ++i) put[i * 16] = a[i];
+    for (int i = 0; i < 8; ++i) s32[i * 32 + lane] = a[i];
     __syncwarp();
     store(p.out1);
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) put[i * 16] = q[i];
+    for (int i = 0; i < 8; ++i) s32[i * 32 + lane] = q[i];
     __syncwarp();
     store(p.out2);
-  } else {
     __syncwarp();
   }
-  if (mine)
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out0) + o) =
-        reinterpret_cast<const uint4*>(st)[lane];
-  __syncwarp();
+  return true;
 }
 
 // The other products: 16 tokens of this warp's 32 features, staged as fp32 so that rows leave in
@@ -400,23 +429,23 @@ __device__ __forceinline__ void finish(const Tile& tl, const GemmParams& p, cons
 
 // Epilogue of a tile: this warp's lane quarter of its FT accumulators from acc on, every kEpiSets-th
 // group of 16 tokens (kSplit: of this CTA's groups, with the other CTAs' partial sums added in rank
-// order) from `set` on. The next group's accumulator columns, and for kHidden its a and q, are under
+// order) from `set` on; false: a wait expired. The next group's accumulator columns, and for kHidden its a and q, are under
 // way while a group is finished; kHidden's first ones come in `in`.
 template <int OP, int BN, int FT, int MODE>
-__device__ __forceinline__ void epilogue(const Tile& tl, int f0, const GemmParams& p, uint32_t acc,
+__device__ __forceinline__ bool epilogue(const Tile& tl, int f0, const GemmParams& p, uint32_t acc,
                                          int quarter, int set, int lane, uint8_t* st,
-                                         const Share& sh, HiddenIn& in) {
+                                         const Share& sh, HiddenIn& in, Exchange& x) {
   using C = GemmCfg<OP, BN, FT, MODE>;
   const int first = (MODE == kSplit ? sh.rank + set * sh.width : set) * 16;
   const int next = (MODE == kSplit ? kEpiSets * sh.width : kEpiSets) * 16;
-  if (first >= tl.n_valid) return;
+  if (first >= tl.n_valid) return true;
   const uint32_t taddr = acc + ((uint32_t)(quarter * 32) << 16);
   uint32_t r[16];
   tmem_ld_32x32b_x16(taddr + (uint32_t)first, r);
 #pragma unroll 1
   for (int j = 0; j < FT; ++j) {
-    const int fw = f0 + j * C::kFeat + quarter * (OP == kUp ? 16 : 32);  // first of this warp
-    const int f = fw + (OP == kUp ? lane & 15 : lane);
+    const int fw = f0 + j * C::kFeat + (OP == kUp ? quarter & 1 : quarter) * 32;  // first of this warp
+    const int f = fw + lane;
     const int64_t bi = (int64_t)tl.e * p.n_out + f;
     const bool f_ok = f < p.n_out;
     const float b0 = p.bias0 != nullptr && f_ok ? bf16_to_f32(p.bias0[bi]) : 0.0f;
@@ -441,7 +470,7 @@ __device__ __forceinline__ void epilogue(const Tile& tl, int f0, const GemmParam
         part += kEpiSets * (kPartChunk / 4);
       }
       if constexpr (OP == kUp) {
-        finish_up(tl, p, v, fw, c0, b0, b1, lane, st);
+        if (!finish_up(tl, p, v, fw, c0, b0, b1, lane, st, x)) return false;
       } else {
         const HiddenIn cur = in;
         if (OP == kHidden && nj < FT)
@@ -450,6 +479,7 @@ __device__ __forceinline__ void epilogue(const Tile& tl, int f0, const GemmParam
       }
     }
   }
+  return true;
 }
 
 template <int OP, int BN, int FT, int MODE>
@@ -488,6 +518,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(B.tempty(a), (MODE == kPair ? 2 : 1) * kEpiWarps);
     }
     mbar_init(B.drain(), 1);
+    for (int w = 0; OP == kUp && w < kEpiWarps; ++w) {
+      mbar_init(B.given(w), 1);
+      mbar_init(B.taken(w), 1);
+    }
     mbar_init(B.part_full(), (width > 1 ? width - 1 : 1) * kEpiWarps);
     mbar_init(B.part_free(), (width > 1 ? width - 1 : 1) * kEpiWarps);
     *abort_flag = 0;
@@ -621,6 +655,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3;  // TMEM lanes this warp may access
     const int set = ew >> 2;
     uint8_t* st = epi_tiles + ew * kEpiTileBytes;
+    const int other = quarter < 2 ? ew - 2 : ew + 2;  // two quarters on (warps 2.. are quarters 2, 3, 0, 1)
+    Exchange x{B, ew, other, reinterpret_cast<const float*>(epi_tiles + other * kEpiTileBytes), 0u,
+               quarter >= 2, abort_flag, p.status};
     int acc = 0;
     uint32_t acc_phase = 0, part_phase = 0;
     for (int t = first; t < total_tiles; t += step) {
@@ -657,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_cluster(cluster_addr(B.part_full(), (rank + s) % width));
         if (!mbar_wait_cluster_warp(B.part_full(), part_phase, abort_flag, p.status)) break;
       }
-      epilogue<OP, BN, FT, MODE>(tl, f0, p, d_tmem, quarter, set, lane, st, sh, in);
+      if (!epilogue<OP, BN, FT, MODE>(tl, f0, p, d_tmem, quarter, set, lane, st, sh, in, x)) break;
       if (MODE == kSplit && width > 1) {
         __syncwarp();
         if (lane == 0)
@@ -854,8 +891,8 @@ cudaError_t enqueue_gated_up_bf16(const GatedFfn& g, void* h, void* saved_a, voi
   if (g.rows_max == 0) return cudaSuccess;
   GemmMaps m;
   GemmParams p{};
-  if (!make_bf16_map_2d(&m.a0, g.w_gate, (int64_t)g.E * g.f, g.d, kBK, 16) ||
-      !make_bf16_map_2d(&m.a1, g.w_up, (int64_t)g.E * g.f, g.d, kBK, 16))
+  if (!make_bf16_map_2d(&m.a0, g.w_gate, (int64_t)g.E * g.f, g.d, kBK, kBM / 2) ||
+      !make_bf16_map_2d(&m.a1, g.w_up, (int64_t)g.E * g.f, g.d, kBK, kBM / 2))
     return cudaErrorInvalidValue;
   if (!token_maps(&m.b0l, &m.b0s, g.x, g.rows_max, g.d)) return cudaErrorInvalidValue;
   m.b1l = m.b0l;
